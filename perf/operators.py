@@ -20,7 +20,7 @@ import torch
 own = False
 
 DEVICE = "cuda"
-WORKSPACE_BYTES = 16 << 20  # the library's workspace for grouped products, zeroed once
+WORKSPACE_BYTES = 40 << 20  # the library's workspace for grouped products, zeroed once
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 TINY = 2.0 ** -126          # the least scale: a block of zeros has it
 
@@ -138,6 +138,13 @@ def _normal(g, std, dtype, *shape):
     return torch.empty(shape, dtype=dtype, device=DEVICE).normal_(0.0, std, generator=g)
 
 
+def _scales(a):
+    """What a block whose largest value is `a` is divided by, and what its codes are made with, each rounded once."""
+    a = a.clamp(min=448 * TINY)
+    top = torch.full_like(a, 448.0)
+    return a / top, top / a
+
+
 def _codes(v, scale):
     return (v * scale).to(torch.float8_e4m3fn)
 
@@ -148,9 +155,8 @@ def _fp8_rows(g, rows, n):
     s = torch.empty(_groups(n), rows, dtype=torch.float32, device=DEVICE)
     for b in range(_groups(n)):
         x = _normal(g, 1.0, torch.float32, rows, min(128, n - 128 * b))
-        a = x.abs().amax(1).clamp(min=448 * TINY)
-        q[:, 128 * b:128 * b + 128] = _codes(x, (448 / a)[:, None])
-        s[b] = a / 448
+        s[b], inv = _scales(x.abs().amax(1))
+        q[:, 128 * b:128 * b + 128] = _codes(x, inv[:, None])
     return q, s
 
 
@@ -163,9 +169,8 @@ def _fp8_weights(g, experts, n_out, n_in):
         w = torch.zeros(experts, rows, 128 * _groups(n_in), dtype=torch.float32, device=DEVICE)
         w[:, :, :n_in] = _normal(g, 0.02, torch.float32, experts, rows, n_in)
         w = w.view(experts, rows, _groups(n_in), 128)
-        a = w.abs().amax((1, 3)).clamp(min=448 * TINY)
-        q[:, 128 * b:128 * b + 128] = _codes(w, (448 / a)[:, None, :, None]).view(experts, rows, -1)[:, :, :n_in]
-        s[:, b] = a / 448
+        s[:, b], inv = _scales(w.abs().amax((1, 3)))
+        q[:, 128 * b:128 * b + 128] = _codes(w, inv[:, None, :, None]).view(experts, rows, -1)[:, :, :n_in]
     return q, s
 
 
@@ -234,9 +239,9 @@ def _plain(s):
         wide = torch.zeros(x.shape[0], 128 * groups, dtype=torch.float32, device=DEVICE)
         wide[:, :x.shape[1]] = x
         wide = wide.view(x.shape[0], groups, 128)
-        a = wide.abs().amax(2).clamp(min=448 * TINY)
-        q = (wide * (448 / a)[:, :, None]).view(x.shape[0], -1)[:, :x.shape[1]]
-        return {"q": q.to(torch.float8_e4m3fn), "s": (a / 448).t().contiguous()}
+        scales, inv = _scales(wide.abs().amax(2))
+        q = _codes(wide, inv[:, :, None]).view(x.shape[0], -1)[:, :x.shape[1]].contiguous()
+        return {"q": q, "s": scales.t().contiguous()}
     at = _slots(s)
     if op == "mm":
         return _rows_out(s, torch.bmm(_by_expert(s, s["x"], at), s["w"][s["active"]].float().transpose(1, 2)), at)
