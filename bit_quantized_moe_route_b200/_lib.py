@@ -40,6 +40,12 @@ class QMatC(ctypes.Structure):
                 ("biases", ctypes.c_void_p)]
 
 
+class GmmDims(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("n_out", ctypes.c_int32), ("n_in", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 _VP = ctypes.c_void_p
@@ -72,6 +78,17 @@ _SIGS = {
     "moe_timing_label": (ctypes.c_char_p, [ctypes.c_int32]),
     "moe_set_ffn_path": (ctypes.c_int32, [ctypes.c_int32]),
     "moe_test_stall_fused_wait": (ctypes.c_int32, [ctypes.c_int32]),
+    "moe_grouped_workspace_size": (ctypes.c_size_t, []),
+    "moe_grouped_mm": (ctypes.c_int, [ctypes.POINTER(GmmDims), _VP, ctypes.c_int64, _VP, _VP, _VP, ctypes.c_int64,
+                                      _VP, ctypes.c_size_t, _VP]),
+    "moe_grouped_mm_dx": (ctypes.c_int, [ctypes.POINTER(GmmDims), _VP, ctypes.c_int64, _VP, _VP, _VP, ctypes.c_int64,
+                                         _VP, ctypes.c_size_t, _VP]),
+    "moe_grouped_mm_dw": (ctypes.c_int, [ctypes.POINTER(GmmDims), _VP, ctypes.c_int64, _VP, ctypes.c_int64, _VP, _VP,
+                                         _VP, ctypes.c_size_t, _VP]),
+    "moe_grouped_mm_fp8": (ctypes.c_int, [ctypes.POINTER(GmmDims), _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP,
+                                          ctypes.c_int64, _VP, ctypes.c_size_t, _VP]),
+    "moe_quant_fp8": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, ctypes.c_int64, _VP, _VP,
+                                     _VP]),
     "moe_hc_sinkhorn_mix": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.c_float, _VP, _VP, _VP, _VP, _VP]),
 }
@@ -257,6 +274,156 @@ def read_noalloc_error(stream=None) -> int:
     code = ctypes.c_int32(0)
     _check(load_library().moe_read_noalloc_error(ctypes.byref(code), _stream(stream)), "moe_read_noalloc_error")
     return code.value
+
+
+# --------------------------------------------------- products grouped by expert
+_GMM_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FP8_TYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def grouped_workspace_size() -> int:
+    return load_library().moe_grouped_workspace_size()
+
+
+def alloc_grouped_workspace(device="cuda") -> torch.Tensor:
+    """Zeroed workspace (uint8) of the grouped products; one for each stream or
+    captured graph that may run at the same time as another."""
+    return torch.zeros(grouped_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def _rows_arg(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """Leading dimension of a [rows, cols] matrix whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
+    if not first.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"expected every tensor on {dev}, got one on {t.device}")
+
+
+def _gmm_dims(dtype, out_dtype, offsets, experts: int, rows: int, n_out: int, n_in: int, ws) -> GmmDims:
+    if out_dtype not in _GMM_TYPES:
+        raise ValueError(f"output type {out_dtype} is not supported (bfloat16, float16, float32)")
+    if dtype is not None and dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"operand type {dtype} is not supported (bfloat16, float16)")
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != experts + 1):
+        raise ValueError(f"expert_offsets must be int32 [{experts + 1}]")
+    if ws.dtype != torch.uint8:
+        raise ValueError("ws must be uint8 (alloc_grouped_workspace)")
+    return GmmDims(0 if dtype is None else _GMM_TYPES[dtype], _GMM_TYPES[out_dtype], experts, rows, n_out, n_in, 0)
+
+
+def _on_device(device, stream, call):
+    """Run call(stream handle) with the tensors' device current, on `stream` or that device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream)
+
+
+def grouped_mm(x, w, expert_offsets, y, ws, stream=None):
+    """moe_grouped_mm: y[r] = w[e] @ x[r] for the rows r of expert e.
+
+    x [R, n_in] and w [E, n_out, n_in] bfloat16 or float16, expert_offsets
+    int32 [E+1] (None with E = 1: every row), y [R, n_out] of x's type or
+    float32.  Rows of x and y may be apart (any row stride)."""
+    if w.dim() != 3 or w.dtype != x.dtype:
+        raise ValueError("w must be [E, n_out, n_in] of x's type")
+    E, n_out, n_in = w.shape
+    R = x.shape[0]
+    ld_x, ld_y = _rows_arg(x, "x", R, n_in), _rows_arg(y, "y", R, n_out)
+    d = _gmm_dims(x.dtype, y.dtype, expert_offsets, E, R, n_out, n_in, ws)
+    _one_device(x, w, expert_offsets, y, ws)
+    lib = load_library()
+    _check(_on_device(x.device, stream, lambda s: lib.moe_grouped_mm(
+        ctypes.byref(d), x.data_ptr(), ld_x, _ptr(w), _ptr(expert_offsets), y.data_ptr(), ld_y, _ptr(ws), ws.numel(),
+        s)), "moe_grouped_mm")
+
+
+def grouped_mm_dx(dy, w, expert_offsets, dx, ws, stream=None):
+    """moe_grouped_mm_dx: dx[r] = w[e].T @ dy[r], the gradient of grouped_mm's rows (dy [R, n_out], dx [R, n_in])."""
+    if w.dim() != 3 or w.dtype != dy.dtype:
+        raise ValueError("w must be [E, n_out, n_in] of dy's type")
+    E, n_out, n_in = w.shape
+    R = dy.shape[0]
+    ld_dy, ld_dx = _rows_arg(dy, "dy", R, n_out), _rows_arg(dx, "dx", R, n_in)
+    d = _gmm_dims(dy.dtype, dx.dtype, expert_offsets, E, R, n_out, n_in, ws)
+    _one_device(dy, w, expert_offsets, dx, ws)
+    lib = load_library()
+    _check(_on_device(dy.device, stream, lambda s: lib.moe_grouped_mm_dx(
+        ctypes.byref(d), dy.data_ptr(), ld_dy, _ptr(w), _ptr(expert_offsets), dx.data_ptr(), ld_dx, _ptr(ws),
+        ws.numel(), s)), "moe_grouped_mm_dx")
+
+
+def grouped_mm_dw(dy, x, expert_offsets, dw, ws, stream=None):
+    """moe_grouped_mm_dw: dw[e] = dy[rows of e].T @ x[rows of e], the gradient of grouped_mm's weights
+    (dw [E, n_out, n_in] of x's type or float32; zeros for an expert without rows)."""
+    if dw.dim() != 3 or x.dtype != dy.dtype:
+        raise ValueError("dw must be [E, n_out, n_in], x and dy of one type")
+    E, n_out, n_in = dw.shape
+    R = dy.shape[0]
+    ld_dy, ld_x = _rows_arg(dy, "dy", R, n_out), _rows_arg(x, "x", R, n_in)
+    d = _gmm_dims(x.dtype, dw.dtype, expert_offsets, E, R, n_out, n_in, ws)
+    _one_device(dy, x, expert_offsets, dw, ws)
+    lib = load_library()
+    _check(_on_device(dy.device, stream, lambda s: lib.moe_grouped_mm_dw(
+        ctypes.byref(d), dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, _ptr(expert_offsets), _ptr(dw), _ptr(ws),
+        ws.numel(), s)), "moe_grouped_mm_dw")
+
+
+def grouped_mm_fp8(x, x_scales, w, w_scales, expert_offsets, y, ws, stream=None):
+    """moe_grouped_mm_fp8: grouped_mm over e4m3 codes with a scale for each block of 128.
+
+    x [R, n_in] and x_scales float32 [ceil(n_in/128), R] as quant_fp8 writes
+    them; w [E, n_out, n_in] and w_scales float32 [E, ceil(n_out/128),
+    ceil(n_in/128)].  Codes are float8_e4m3fn or uint8 tensors.
+    expert_offsets None with E = 1: one matrix for every row.  y bfloat16,
+    float16 or float32 [R, n_out]."""
+    if w.dim() != 3 or w.dtype not in _FP8_TYPES or x.dtype not in _FP8_TYPES:
+        raise ValueError("x and w must be e4m3 codes (float8_e4m3fn or uint8), w [E, n_out, n_in]")
+    E, n_out, n_in = w.shape
+    R = x.shape[0]
+    gi, go = (n_in + 127) // 128, (n_out + 127) // 128
+    if x_scales.dtype != torch.float32 or tuple(x_scales.shape) != (gi, R):
+        raise ValueError(f"x_scales must be float32 [{gi}, {R}]")
+    if w_scales.dtype != torch.float32 or tuple(w_scales.shape) != (E, go, gi):
+        raise ValueError(f"w_scales must be float32 [{E}, {go}, {gi}]")
+    ld_x, ld_y = _rows_arg(x, "x", R, n_in), _rows_arg(y, "y", R, n_out)
+    d = _gmm_dims(None, y.dtype, expert_offsets, E, R, n_out, n_in, ws)
+    _one_device(x, x_scales, w, w_scales, expert_offsets, y, ws)
+    lib = load_library()
+    _check(_on_device(x.device, stream, lambda s: lib.moe_grouped_mm_fp8(
+        ctypes.byref(d), x.data_ptr(), ld_x, _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(expert_offsets),
+        y.data_ptr(), ld_y, _ptr(ws), ws.numel(), s)), "moe_grouped_mm_fp8")
+
+
+def quant_fp8(x, codes, scales, stream=None):
+    """moe_quant_fp8: x bfloat16 or float16 [R, n_in] (any row stride) to codes [R, n_in] (float8_e4m3fn or uint8)
+    and scales float32 [ceil(n_in/128), R], one for each 128 inputs of a row."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"type {x.dtype} is not supported (bfloat16, float16)")
+    if x.dim() != 2 or codes.dtype not in _FP8_TYPES or codes.shape != x.shape:
+        raise ValueError("x must be [R, n_in], codes float8_e4m3fn or uint8 of the same shape")
+    R, n_in = x.shape
+    if scales.dtype != torch.float32 or tuple(scales.shape) != ((n_in + 127) // 128, R):
+        raise ValueError(f"scales must be float32 [{(n_in + 127) // 128}, {R}]")
+    ld = _rows_arg(x, "x", R, n_in)
+    _one_device(x, codes, scales)
+    lib = load_library()
+    _check(_on_device(x.device, stream, lambda s: lib.moe_quant_fp8(
+        _GMM_TYPES[x.dtype], R, n_in, x.data_ptr(), ld, _ptr(codes), _ptr(scales), s)), "moe_quant_fp8")
 
 
 FFN_AUTO, FFN_GEMV, FFN_TENSOR_CORE, FFN_DECODE_FUSED = 0, 1, 2, 3

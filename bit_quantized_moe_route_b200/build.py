@@ -33,7 +33,7 @@ def sources():
 
 def inputs():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
-        glob.glob(os.path.join(CSRC, "*.inl"))) + [os.path.join(ROOT, "include", "moe_lowbit.h")]
+        glob.glob(os.path.join(CSRC, "*.inl"))) + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(ROOT, "include", "moe_lowbit.h")]
 
 
 def up_to_date() -> bool:

@@ -1,0 +1,274 @@
+// Host side of the grouped products and of the 8-bit row quantiser declared in
+// include/moe_lowbit.h: argument validation and kernel launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "api_util.h"
+#include "grouped_any.cuh"
+#include "quant_fp8.cuh"
+
+using namespace moe;
+
+namespace {
+
+constexpr size_t kGmmWsBytes = size_t(40) << 20;
+
+#define GMM_TRY(call)                    \
+  do {                                   \
+    const moe_status_t st_ = (call);     \
+    if (st_ != MOE_OK) return st_;       \
+  } while (0)
+
+int sm_count(int* sms) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  int v = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (!v) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (dev < 64) cached[dev].store(v, std::memory_order_relaxed);
+  }
+  *sms = v;
+  return 0;
+}
+
+size_t type_bytes(int t) { return t == G_FP32 ? 4 : t == G_E4M3 ? 1 : 2; }
+
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+// `rows` rows of n elements, ld elements apart
+size_t span_bytes(long long rows, long long ld, long long n, int type) {
+  return rows > 0 ? ((size_t)(rows - 1) * ld + n) * type_bytes(type) : 0;
+}
+moe_status_t check_apart(const Span& out, const Span* in, int n) {
+  const uintptr_t a = (uintptr_t)out.p, b = a + out.bytes;
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t c = (uintptr_t)in[i].p, d = c + in[i].bytes;
+    if (in[i].p && out.bytes && in[i].bytes && a < d && c < b)
+      return api_fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in[i].name);
+  }
+  return MOE_OK;
+}
+
+moe_status_t check_aligned(const Span& s, size_t unit) {
+  if ((uintptr_t)s.p % unit) return api_fail(MOE_ERR_INVALID_ARG, "%s is not aligned to its elements", s.name);
+  return MOE_OK;
+}
+
+moe_status_t check_gmm_dims(const moe_gmm_dims_t* d, bool fp8, bool have_offsets) {
+  if (!d) return api_fail(MOE_ERR_INVALID_ARG, "dims is NULL");
+  if (!fp8 && d->dtype != MOE_BF16 && d->dtype != MOE_FP16)
+    return api_fail(MOE_ERR_UNSUPPORTED, "dtype=%d not in {0 (bf16), 1 (fp16)}", d->dtype);
+  if (d->out_dtype != MOE_BF16 && d->out_dtype != MOE_FP16 && d->out_dtype != MOE_FP32)
+    return api_fail(MOE_ERR_UNSUPPORTED, "out_dtype=%d not in {0 (bf16), 1 (fp16), 2 (fp32)}", d->out_dtype);
+  if (!fp8 && d->out_dtype != MOE_FP32 && d->out_dtype != d->dtype)
+    return api_fail(MOE_ERR_UNSUPPORTED, "out_dtype must be dtype or fp32");
+  if (d->n_experts < 1 || d->n_experts > kGmmMaxExperts)
+    return api_fail(MOE_ERR_INVALID_ARG, "n_experts=%d outside [1, %d]", d->n_experts, kGmmMaxExperts);
+  if (!have_offsets && d->n_experts != 1)
+    return api_fail(MOE_ERR_INVALID_ARG, "expert_offsets is NULL with n_experts=%d", d->n_experts);
+  if (d->n_out < 1 || d->n_out > 65536 || d->n_in < 1 || d->n_in > 65536)
+    return api_fail(MOE_ERR_INVALID_ARG, "n_out=%d or n_in=%d outside [1, 65536]", d->n_out, d->n_in);
+  if (d->rows < 0 || d->rows > (1 << 30)) return api_fail(MOE_ERR_INVALID_ARG, "rows=%d outside [0, 2^30]", d->rows);
+  if (d->reserved) return api_fail(MOE_ERR_INVALID_ARG, "reserved must be 0");
+  return MOE_OK;
+}
+
+moe_status_t check_ld(long long ld, int n, const char* name) {
+  if (ld < n || ld > (1LL << 31))
+    return api_fail(MOE_ERR_INVALID_ARG, "%s=%lld outside [%d, 2^31]", name, ld, n);
+  return MOE_OK;
+}
+
+moe_status_t check_gmm_ws(void* ws, size_t ws_bytes) {
+  if (!ws) return api_fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if ((uintptr_t)ws % 256) return api_fail(MOE_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  if (ws_bytes < kGmmWsBytes)
+    return api_fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", ws_bytes, kGmmWsBytes);
+  return api_check_dev_ptr(ws, "workspace");
+}
+
+template <int OP, int IN>
+moe_status_t launch_any(const GmmProblem& p, cudaStream_t s, int sms) {
+  const long long m_tiles = ((OP == G_MM ? p.n_out : p.n_in) + kGaTile - 1) / kGaTile;
+  const long long n_tiles = OP == G_DW ? (long long)p.E * ((p.n_out + kGaTile - 1) / kGaTile)
+                                       : (p.rows + kGaTile - 1) / kGaTile + std::min(p.E, p.rows);
+  const int grid = (int)std::min<long long>(m_tiles * n_tiles, (long long)sms * 5);
+  grouped_any_kernel<OP, IN><<<grid, kGaThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "grouped_any_kernel: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+template <int OP>
+moe_status_t run_gmm(const GmmProblem& p, int in_type, cudaStream_t s) {
+  int sms = 0;
+  if (sm_count(&sms)) return api_fail(MOE_ERR_CUDA, "device query failed");
+  if (in_type == G_BF16) return launch_any<OP, G_BF16>(p, s, sms);
+  if (in_type == G_FP16) return launch_any<OP, G_FP16>(p, s, sms);
+  if constexpr (OP == G_MM) return launch_any<OP, G_E4M3>(p, s, sms);
+  return api_fail(MOE_ERR_UNSUPPORTED, "type");
+}
+
+// The products over rows: mm (rows_in = x) and dx (rows_in = dy).
+template <int OP>
+moe_status_t rows_product(const moe_gmm_dims_t* d, const char* in_name, const void* in, int64_t ld_in, const void* w,
+                          const int32_t* off, const char* out_name, void* out, int64_t ld_out, const float* sx,
+                          const float* sw, bool fp8, void* ws, size_t ws_bytes, void* stream) {
+  api_clear_detail();
+  GMM_TRY(check_gmm_dims(d, fp8, off != nullptr));
+  const int in_cols = OP == G_MM ? d->n_in : d->n_out, out_cols = OP == G_MM ? d->n_out : d->n_in;
+  GMM_TRY(check_ld(ld_in, in_cols, OP == G_MM ? "ld_x" : "ld_dy"));
+  GMM_TRY(check_ld(ld_out, out_cols, OP == G_MM ? "ld_y" : "ld_dx"));
+  if (d->rows == 0) return MOE_OK;
+  const int type = fp8 ? G_E4M3 : d->dtype;
+  const long long groups = (d->n_in + 127) / 128;
+  const Span ins[5] = {
+      {in_name, in, span_bytes(d->rows, ld_in, in_cols, type)},
+      {"w", w, span_bytes((long long)d->n_experts * d->n_out, d->n_in, d->n_in, type)},
+      {"expert_offsets", off, off ? sizeof(int) * (size_t)(d->n_experts + 1) : 0},
+      {"x_scales", sx, fp8 ? sizeof(float) * (size_t)(groups * d->rows) : 0},
+      {"w_scales", sw, fp8 ? sizeof(float) * (size_t)(groups * d->n_experts * ((d->n_out + 127) / 128)) : 0}};
+  const Span o = {out_name, out, span_bytes(d->rows, ld_out, out_cols, d->out_dtype)};
+  GMM_TRY(check_gmm_ws(ws, ws_bytes));
+  for (const Span& s : ins)
+    if (s.p || s.bytes) GMM_TRY(api_check_dev_ptr(s.p, s.name));
+  GMM_TRY(api_check_dev_ptr(out, out_name));
+  GMM_TRY(check_aligned(ins[0], type_bytes(type)));
+  GMM_TRY(check_aligned(ins[1], type_bytes(type)));
+  GMM_TRY(check_aligned(ins[2], 4));
+  GMM_TRY(check_aligned(ins[3], 4));
+  GMM_TRY(check_aligned(ins[4], 4));
+  GMM_TRY(check_aligned(o, type_bytes(d->out_dtype)));
+  GMM_TRY(check_apart(o, ins, 5));
+  const Span wsp = {"ws", ws, ws_bytes};
+  GMM_TRY(check_apart(o, &wsp, 1));
+  GmmProblem p{};
+  p.w = w;
+  p.rows_in = in;
+  p.ld_rows = ld_in;
+  p.off = off;
+  p.out = out;
+  p.ld_out = ld_out;
+  p.sx = sx;
+  p.sw = sw;
+  p.out_type = d->out_dtype;
+  p.E = d->n_experts;
+  p.rows = d->rows;
+  p.n_out = d->n_out;
+  p.n_in = d->n_in;
+  p.err = reinterpret_cast<int*>(ws);
+  return run_gmm<OP>(p, type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grouped_workspace_size(void) { return kGmmWsBytes; }
+
+moe_status_t moe_grouped_mm(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const void* w,
+                            const int32_t* expert_offsets, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                            void* stream) {
+  return rows_product<G_MM>(dims, "x", x, ld_x, w, expert_offsets, "y", y, ld_y, nullptr, nullptr, false, ws, ws_bytes,
+                            stream);
+}
+
+moe_status_t moe_grouped_mm_dx(const moe_gmm_dims_t* dims, const void* dy, int64_t ld_dy, const void* w,
+                               const int32_t* expert_offsets, void* dx, int64_t ld_dx, void* ws, size_t ws_bytes,
+                               void* stream) {
+  return rows_product<G_DX>(dims, "dy", dy, ld_dy, w, expert_offsets, "dx", dx, ld_dx, nullptr, nullptr, false, ws,
+                            ws_bytes, stream);
+}
+
+moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                               const int32_t* expert_offsets, void* dw, void* ws, size_t ws_bytes, void* stream) {
+  api_clear_detail();
+  GMM_TRY(check_gmm_dims(dims, false, expert_offsets != nullptr));
+  const moe_gmm_dims_t& d = *dims;
+  GMM_TRY(check_ld(ld_dy, d.n_out, "ld_dy"));
+  GMM_TRY(check_ld(ld_x, d.n_in, "ld_x"));
+  const Span ins[3] = {{"dy", dy, span_bytes(d.rows, ld_dy, d.n_out, d.dtype)},
+                       {"x", x, span_bytes(d.rows, ld_x, d.n_in, d.dtype)},
+                       {"expert_offsets", expert_offsets, expert_offsets ? sizeof(int) * (size_t)(d.n_experts + 1) : 0}};
+  const Span o = {"dw", dw, span_bytes((long long)d.n_experts * d.n_out, d.n_in, d.n_in, d.out_dtype)};
+  GMM_TRY(check_gmm_ws(ws, ws_bytes));
+  for (const Span& s : ins)
+    if (s.bytes) GMM_TRY(api_check_dev_ptr(s.p, s.name));
+  GMM_TRY(api_check_dev_ptr(dw, "dw"));
+  GMM_TRY(check_aligned(ins[0], 2));
+  GMM_TRY(check_aligned(ins[1], 2));
+  GMM_TRY(check_aligned(ins[2], 4));
+  GMM_TRY(check_aligned(o, type_bytes(d.out_dtype)));
+  GMM_TRY(check_apart(o, ins, 3));
+  const Span wsp = {"ws", ws, ws_bytes};
+  GMM_TRY(check_apart(o, &wsp, 1));
+  GmmProblem p{};
+  p.rows_in = dy;
+  p.x = x;
+  p.ld_rows = ld_dy;
+  p.ld_x = ld_x;
+  p.off = expert_offsets;
+  p.out = dw;
+  p.out_type = d.out_dtype;
+  p.E = d.n_experts;
+  p.rows = d.rows;
+  p.n_out = d.n_out;
+  p.n_in = d.n_in;
+  p.err = reinterpret_cast<int*>(ws);
+  return run_gmm<G_DW>(p, d.dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_grouped_mm_fp8(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const float* x_scales,
+                                const void* w, const float* w_scales, const int32_t* expert_offsets, void* y,
+                                int64_t ld_y, void* ws, size_t ws_bytes, void* stream) {
+  return rows_product<G_MM>(dims, "x", x, ld_x, w, expert_offsets, "y", y, ld_y, x_scales, w_scales, true, ws, ws_bytes,
+                            stream);
+}
+
+moe_status_t moe_quant_fp8(int32_t dtype, int32_t rows, int32_t n_in, const void* x, int64_t ld_x, void* codes,
+                           float* scales, void* stream) {
+  api_clear_detail();
+  if (dtype != MOE_BF16 && dtype != MOE_FP16)
+    return api_fail(MOE_ERR_UNSUPPORTED, "dtype=%d not in {0 (bf16), 1 (fp16)}", dtype);
+  if (n_in < 1 || n_in > 65536) return api_fail(MOE_ERR_INVALID_ARG, "n_in=%d outside [1, 65536]", n_in);
+  if (rows < 0 || rows > (1 << 30)) return api_fail(MOE_ERR_INVALID_ARG, "rows=%d outside [0, 2^30]", rows);
+  GMM_TRY(check_ld(ld_x, n_in, "ld_x"));
+  if (rows == 0) return MOE_OK;
+  const Span in = {"x", x, span_bytes(rows, ld_x, n_in, dtype)};
+  const Span o1 = {"codes", codes, (size_t)rows * n_in};
+  const Span o2 = {"scales", scales, (size_t)rows * ((n_in + 127) / 128) * 4};
+  GMM_TRY(api_check_dev_ptr(x, "x"));
+  GMM_TRY(api_check_dev_ptr(codes, "codes"));
+  GMM_TRY(api_check_dev_ptr(scales, "scales"));
+  GMM_TRY(check_aligned(in, 2));
+  GMM_TRY(check_aligned(o2, 4));
+  GMM_TRY(check_apart(o1, &in, 1));
+  GMM_TRY(check_apart(o2, &in, 1));
+  GMM_TRY(check_apart(o1, &o2, 1));
+  int sms = 0;
+  if (sm_count(&sms)) return api_fail(MOE_ERR_CUDA, "device query failed");
+  const bool vec = n_in % 16 == 0 && ld_x % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 16 == 0;
+  const int gy = (n_in + kQfCols - 1) / kQfCols;
+  const dim3 grid((unsigned)std::min((rows + kQfRows - 1) / kQfRows, std::max(1, sms * 64 / gy)), (unsigned)gy);
+  const uint16_t* xp = reinterpret_cast<const uint16_t*>(x);
+  uint8_t* q = reinterpret_cast<uint8_t*>(codes);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == MOE_BF16) {
+    if (vec) quant_fp8_kernel<G_BF16, true><<<grid, kQfThreads, 0, s>>>(xp, ld_x, rows, n_in, q, scales);
+    else quant_fp8_kernel<G_BF16, false><<<grid, kQfThreads, 0, s>>>(xp, ld_x, rows, n_in, q, scales);
+  } else {
+    if (vec) quant_fp8_kernel<G_FP16, true><<<grid, kQfThreads, 0, s>>>(xp, ld_x, rows, n_in, q, scales);
+    else quant_fp8_kernel<G_FP16, false><<<grid, kQfThreads, 0, s>>>(xp, ld_x, rows, n_in, q, scales);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "quant_fp8_kernel: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/moe_lowbit.h"
+#include "api_util.h"
 #include "common.cuh"
 #include "ffn_gemv.cuh"
 #include "stream_types.cuh"
@@ -1563,3 +1564,39 @@ extern "C" moe_status_t moe_dequant_mxfp8(const void* codes, const uint8_t* scal
   MOE_CHECK_LAUNCH("dequant_mxfp8_kernel");
   return MOE_OK;
 }
+
+// ---- helpers of the other translation units (api_util.h)
+namespace moe {
+
+moe_status_t api_fail(moe_status_t st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+void api_clear_detail() { g_detail[0] = 0; }
+
+moe_status_t api_check_dev_ptr(const void* p, const char* name) { return check_dev_ptr(p, name); }
+
+moe_status_t api_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,
+                            const uint64_t* strides, const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t d[3], s[2];
+  cuuint32_t b[3], es[3];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i) s[i - 1] = strides[i - 1];
+  }
+  const CUresult r = enc(m, dt, (cuuint32_t)rank, const_cast<void*>(ptr), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MOE_OK;
+}
+
+}  // namespace moe

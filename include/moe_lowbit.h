@@ -324,6 +324,118 @@ moe_status_t moe_dequant_mxfp8(const void* codes, const uint8_t* scales, int64_t
                                void* stream);
 
 /*
+ * Products grouped by expert over weights that are not packed: the 16-bit
+ * source weights of a layer (to calibrate, fine-tune or recover a quantised
+ * or pruned one) and 8-bit weights as FP8 checkpoints store them [PR1192 FP8
+ * re-quantisation thread: e4m3 bytes with one scale per 128x128 block].
+ *
+ *   rows      : input rows in expert order, as moe_permute orders the pairs:
+ *               expert e owns rows [off[e], off[e+1]).  Output rows that
+ *               belong to no expert (before off[0], from off[n_experts] on)
+ *               are left as they were.
+ *   dtype     : moe_dtype_t of x, dy and w (MOE_BF16 or MOE_FP16; not used
+ *               by moe_grouped_mm_fp8)
+ *   out_dtype : type of the output: dtype or MOE_FP32; any of the three for
+ *               moe_grouped_mm_fp8.  Sums are fp32 and are rounded once, to
+ *               nearest even; a sum beyond fp16 becomes infinite there.
+ *   reserved  : 0
+ * Limits: 1 <= n_experts <= 1024, 1 <= n_out, n_in <= 65536,
+ * 0 <= rows <= 2^30.
+ */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
+typedef struct {
+  int32_t dtype;
+  int32_t out_dtype;
+  int32_t n_experts;
+  int32_t rows;
+  int32_t n_out;
+  int32_t n_in;
+  int32_t reserved;
+} moe_gmm_dims_t;
+
+/*
+ * Bytes of the workspace of the four grouped products (one size for all
+ * dims).  As for the other entry points: caller-owned device memory, 256-byte
+ * aligned, zeroed once before first use (and again after MOE_ERR_TIMEOUT),
+ * not shared by calls that overlap on the GPU -- two streams, or two captured
+ * graphs that may run at the same time, need one each.  Its first word is the
+ * device error word (moe_read_device_error).
+ */
+size_t moe_grouped_workspace_size(void);
+
+/*
+ * y[r] = W[e] . x[r] for every row r of expert e.
+ *   x  : [rows, n_in], ld_x >= n_in elements between rows
+ *   w  : [n_experts, n_out, n_in]
+ *   expert_offsets : int32 [n_experts+1], 0 <= off[0] <= ... <=
+ *        off[n_experts] <= rows, checked on the device: a violation records
+ *        MOE_ERR_DEVICE_INPUT and nothing is written.  NULL with n_experts =
+ *        1: one matrix for every row.
+ *   y  : [rows, n_out] (out), ld_y >= n_out; overlaps no input
+ * Pointers are aligned to their elements.  Operands whose base address and
+ * row stride (and, for the weights, row length) are multiples of 16 bytes run
+ * on the tcgen05 kernel, others on a slower one with the same results up to
+ * the order of the fp32 sums.  Results do not depend on what else runs: the
+ * same call gives the same bits.
+ */
+moe_status_t moe_grouped_mm(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const void* w,
+                            const int32_t* expert_offsets, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * The gradient of moe_grouped_mm with respect to its rows:
+ * dx[r] = W[e]^T . dy[r].
+ *   dy : [rows, n_out], ld_dy >= n_out;  dx : [rows, n_in] (out), ld_dx >= n_in
+ * Otherwise as moe_grouped_mm.
+ */
+moe_status_t moe_grouped_mm_dx(const moe_gmm_dims_t* dims, const void* dy, int64_t ld_dy, const void* w,
+                               const int32_t* expert_offsets, void* dx, int64_t ld_dx, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * The gradient of moe_grouped_mm with respect to its weights:
+ * dw[e] = sum over the rows r of expert e of dy[r] x[r]^T, zeros for an
+ * expert without rows.
+ *   dw : [n_experts, n_out, n_in] (out)
+ * Otherwise as moe_grouped_mm (with rows = 0, dw is still written).
+ */
+moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                               const int32_t* expert_offsets, void* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_grouped_mm over e4m3 operands with a scale for each block of 128:
+ *   y[r, o] = sum_g x_scales[g, r] * w_scales[e, o/128, g]
+ *                   * sum_{i in group g} x[r, i] * w[e, o, i]
+ *   x        : e4m3 [rows, n_in], ld_x >= n_in bytes between rows
+ *   x_scales : fp32 [ceil(n_in/128), rows], as moe_quant_fp8 writes them
+ *   w        : e4m3 [n_experts, n_out, n_in]
+ *   w_scales : fp32 [n_experts, ceil(n_out/128), ceil(n_in/128)] (e8m0 block
+ *              scales of a checkpoint widen to fp32 exactly)
+ * The sums of a group are taken over exact products; scales may be any fp32
+ * values.  Otherwise as moe_grouped_mm.
+ */
+moe_status_t moe_grouped_mm_fp8(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const float* x_scales,
+                                const void* w, const float* w_scales, const int32_t* expert_offsets, void* y,
+                                int64_t ld_y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rows to 8 bits with one scale for each group of 128 inputs (the last group
+ * of a row may be shorter):
+ *   a = max(largest |x| of the group, 448 * 2^-126)
+ *   scales[g, r] = a / 448,  codes[r, i] = e4m3(x[r, i] * (448 / a))
+ * each quotient and product rounded once to fp32, the code to nearest even.
+ * A group that holds an infinity or a NaN gets NaN codes or a scale that is
+ * not finite, so that what is computed from it is NaN.
+ *   dtype  : MOE_BF16 or MOE_FP16
+ *   x      : [rows, n_in], ld_x >= n_in elements between rows
+ *   codes  : e4m3 [rows, n_in] (out);  scales : fp32 [ceil(n_in/128), rows] (out)
+ * 0 <= rows <= 2^30, 1 <= n_in <= 65536.  One launch, no workspace; outputs
+ * overlap neither the input nor each other.
+ */
+moe_status_t moe_quant_fp8(int32_t dtype, int32_t rows, int32_t n_in, const void* x, int64_t ld_x, void* codes,
+                           float* scales, void* stream);
+
+/*
  * mHC residual mixing, fused (the block next to the MoE layer in each
  * DeepSeek-V4 layer) [CARD-4BIT Architecture "mHC": hc_mult parallel copies
  * of the hidden state recombined by a doubly-stochastic, Sinkhorn-normalised

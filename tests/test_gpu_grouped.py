@@ -1,0 +1,545 @@
+"""Grouped products (forward, gradients, 8-bit) and the 8-bit row quantiser
+against plain sums in 64 bits.
+
+Tolerances, from the arithmetic alone.  Products of 16-bit or e4m3 operands are
+exact in fp32.  A sum of n of them in fp32, in any order and with every
+partial sum rounded or truncated, is off by at most n * 2^-23 * S, where S is
+the sum of the products' magnitudes (a truncation is off by less than one step,
+2^-23 of the partial sum, and each partial sum is at most S).  Rounding to the
+output's type adds eps / 2 of the value (half its smallest subnormal step for
+results near zero).  The 8-bit product's two scale multiplications add 2^-23
+each, inside the same count (n + 4)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_moe_route_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ws(cuda_device):
+    return moe.alloc_grouped_workspace(cuda_device)
+
+
+def gen(seed, dev):
+    g = torch.Generator(device=dev)
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, dtype, *shape, std=1.0):
+    return torch.empty(shape, dtype=dtype, device=g.device).normal_(0.0, std, generator=g)
+
+
+def offsets_of(counts, dev, start=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]) + start, dtype=torch.int32, device=dev)
+
+
+def strided(g, dtype, rows, cols, pad, shift=0):
+    """[rows, cols] with `pad` more elements per row, `shift` elements into its buffer."""
+    buf = normal(g, dtype, rows * (cols + pad) + shift)
+    return buf[shift:].view(rows, cols + pad)[:, :cols]
+
+
+def close(got, ref, mag, n, label=""):
+    """got against the 64-bit ref; mag = sum of the products' magnitudes, n = how many there are."""
+    eps = torch.finfo(got.dtype).eps / 2 if got.dtype != FP else 2.0 ** -24
+    tiny = torch.finfo(got.dtype).smallest_normal * torch.finfo(got.dtype).eps
+    tol = (n + 4) * 2.0 ** -23 * mag * (1 + eps) + eps * ref.abs() + tiny
+    err = (got.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), (label, int(bad.sum()), (err / tol).nan_to_num(1e9).max().item(),
+                                 bad.nonzero()[:4].tolist())
+
+
+def reference(op, a, b, off, experts):
+    """(values, magnitudes) in 64 bits over the whole output; rows of no expert are NaN."""
+    off = [0, a.shape[0]] if off is None else off.tolist()
+    a, b = a.double(), b.double()
+    if op == "dw":
+        out = torch.zeros(experts, a.shape[1], b.shape[1], dtype=torch.float64, device=a.device)
+        mag = torch.zeros_like(out)
+        for e in range(experts):
+            u, v = a[off[e]:off[e + 1]], b[off[e]:off[e + 1]]
+            out[e], mag[e] = u.t() @ v, u.abs().t() @ v.abs()
+        return out, mag
+    cols = b.shape[1] if op == "mm" else b.shape[2]
+    out = torch.full((a.shape[0], cols), float("nan"), dtype=torch.float64, device=a.device)
+    mag = torch.zeros_like(out)
+    for e in range(experts):
+        w = b[e].t() if op == "mm" else b[e]
+        u = a[off[e]:off[e + 1]]
+        out[off[e]:off[e + 1]], mag[off[e]:off[e + 1]] = u @ w, u.abs() @ w.abs()
+    return out, mag
+
+
+def run_op(op, counts, n_in, n_out, dtype, out, dev, ws, pad=0, start=0, ld_pad=0, shift=0, seed=0, dense=False):
+    """One call on random inputs, checked whole: values, rows of no expert, and no device error."""
+    g = gen(seed + 1000 * n_in + n_out, dev)
+    experts, rows = len(counts), start + int(sum(counts)) + pad
+    off = None if dense else offsets_of(counts, dev, start)
+    w = normal(g, dtype, experts * n_out * n_in + shift, std=0.05)[shift:].view(experts, n_out, n_in)
+    x, dy = strided(g, dtype, rows, n_in, ld_pad, shift), strided(g, dtype, rows, n_out, ld_pad, shift)
+    if op == "dw":
+        y = torch.full((experts, n_out, n_in), 7.0, dtype=out, device=dev)
+        moe.grouped_mm_dw(dy, x, off, y, ws)
+        n = torch.tensor(counts, device=dev, dtype=torch.float64)[:, None, None]
+    else:
+        cols = n_out if op == "mm" else n_in
+        y = torch.full((rows, cols + ld_pad), 7.0, dtype=out, device=dev)[:, :cols]
+        if op == "mm":
+            moe.grouped_mm(x, w, off, y, ws)
+        else:
+            moe.grouped_mm_dx(dy, w, off, y, ws)
+        n = n_in if op == "mm" else n_out
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    ref, mag = reference(op, dy if op != "mm" else x, x if op == "dw" else w, off, experts)
+    label = (op, counts, n_in, n_out)
+    if op == "dw":
+        close(y, ref, mag, n, label)
+    else:
+        inside = torch.zeros(rows, dtype=torch.bool, device=dev)
+        inside[start:rows - pad] = True
+        close(y[inside], ref[inside], mag[inside], n, label)
+        assert bool((y[~inside] == 7.0).all())
+        assert ld_pad == 0 or bool((y.as_strided((rows, ld_pad), (cols + ld_pad, 1), cols) == 7.0).all())
+    return y
+
+
+OPS = ["mm", "dx", "dw"]
+RAGGED = [0, 1, 5, 0, 17, 64, 65, 130, 0]
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, HF), (BF, FP), (HF, FP)])
+@pytest.mark.parametrize("n_in,n_out", [(256, 128), (64, 320), (72, 40), (8, 8), (136, 264)])
+def test_ragged(cuda_device, ws, op, dtype, out, n_in, n_out):
+    run_op(op, RAGGED, n_in, n_out, dtype, out, cuda_device, ws)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("n_in,n_out", [(1, 1), (33, 100), (257, 129), (100, 64), (64, 100), (7, 300)])
+def test_odd_widths(cuda_device, ws, op, n_in, n_out):
+    run_op(op, RAGGED, n_in, n_out, BF, BF, cuda_device, ws)
+    run_op(op, [3], n_in, n_out, HF, FP, cuda_device, ws, dense=True)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("counts", [[1], [0], [0, 0, 0], [1, 0, 0, 1], [256], [257], [511, 0, 513], [16] * 40, [1] * 300,
+                                    [2000]])
+def test_row_counts(cuda_device, ws, op, counts):
+    run_op(op, counts, 192, 256, BF, FP, cuda_device, ws)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("ld_pad,shift", [(8, 0), (24, 8), (3, 0), (0, 1), (5, 3)])
+def test_strides_and_alignment(cuda_device, ws, op, ld_pad, shift):
+    run_op(op, [5, 0, 70, 33], 128, 192, BF, BF, cuda_device, ws, ld_pad=ld_pad, shift=shift)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("pad,start", [(1, 0), (77, 0), (0, 5), (300, 130)])
+def test_rows_of_no_expert_stay(cuda_device, ws, op, pad, start):
+    run_op(op, [9, 0, 140, 1], 128, 256, HF, HF, cuda_device, ws, pad=pad, start=start)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_one_matrix_without_offsets(cuda_device, ws, op):
+    for rows in (1, 2, 31, 300):
+        run_op(op, [rows], 512, 384, BF, BF, cuda_device, ws, dense=True, seed=rows)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_long_sums_of_few_outputs(cuda_device, ws, op):
+    """Few outputs and a long contracted dimension: the work is split along it."""
+    counts = [1, 3] if op != "dw" else [9000, 1, 4100]
+    wide = {"mm": (8192, 64), "dx": (64, 8192), "dw": (64, 72)}[op]
+    run_op(op, counts, *wide, BF, FP, cuda_device, ws)
+    run_op(op, counts, *wide, HF, HF, cuda_device, ws)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_many_experts(cuda_device, ws, op):
+    counts = np.random.default_rng(4).integers(0, 4, 1024).tolist()
+    run_op(op, counts, 64, 72, BF, BF, cuda_device, ws)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("aligned", [True, False])
+def test_same_bits_every_time(cuda_device, ws, op, aligned):
+    n_in = 2048 if aligned else 2047
+    a = run_op(op, [3, 40, 0, 7], n_in, 320, BF, FP, cuda_device, ws)
+    for _ in range(3):
+        assert torch.equal(a, run_op(op, [3, 40, 0, 7], n_in, 320, BF, FP, cuda_device, ws))
+
+
+@pytest.mark.parametrize("n_in", [128, 100])
+def test_nothing_leaks_between_experts(cuda_device, ws, n_in):
+    """NaN and infinity in rows of no expert, in another expert's rows and in weights without rows stay there."""
+    g = gen(3, cuda_device)
+    counts, n_out = [5, 0, 20, 9], 136
+    off = offsets_of(counts, cuda_device)
+    x, dy = normal(g, BF, 50, n_in), normal(g, BF, 50, n_out)
+    w = normal(g, BF, 4, n_out, n_in)
+    clean_x, clean_dy, clean_w = x.clone(), dy.clone(), w.clone()
+    for t in (x, dy):
+        t[34:] = float("nan")
+        t[5:25] = float("inf")
+    w[1] = float("nan")
+    w[2, 0, 0] = float("inf")
+    keep = [r for r in range(34) if not 5 <= r < 25]
+    for op, a, ca, cols in (("mm", x, clean_x, n_out), ("dx", dy, clean_dy, n_in)):
+        y = torch.zeros(50, cols, dtype=FP, device=cuda_device)
+        (moe.grouped_mm if op == "mm" else moe.grouped_mm_dx)(a, w, off, y, ws)
+        ref, mag = reference(op, ca, clean_w, off, 4)
+        close(y[keep], ref[keep], mag[keep], n_in if op == "mm" else n_out, op)
+        assert bool((~torch.isfinite(y[5:25])).all()) and bool((y[34:] == 0).all())
+    dw = torch.empty(4, n_out, n_in, dtype=FP, device=cuda_device)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    ref, mag = reference("dw", clean_dy, clean_x, off, 4)
+    for e in (0, 1, 3):
+        close(dw[e], ref[e], mag[e], 50, ("dw", e))
+    assert not bool(torch.isfinite(dw[2]).any())
+    assert moe.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("n_in", [128, 127])
+def test_bad_offsets(cuda_device, ws, n_in):
+    x, w = torch.ones(20, n_in, dtype=BF, device=cuda_device), torch.ones(3, 64, n_in, dtype=BF, device=cuda_device)
+    dy = torch.ones(20, 64, dtype=BF, device=cuda_device)
+    for bad in ([-1, 3, 5, 9], [0, 5, 4, 9], [0, 5, 9, 21], [0, 2 ** 31 - 1, 3, 4], [5, 2, 9, 20], [0, 0, 0, -2 ** 31]):
+        off = torch.tensor(bad, dtype=torch.int32, device=cuda_device)
+        y = torch.full((20, 64), 7.0, dtype=BF, device=cuda_device)
+        dx = torch.full((20, n_in), 7.0, dtype=BF, device=cuda_device)
+        dw = torch.full((3, 64, n_in), 7.0, dtype=BF, device=cuda_device)
+        for call, out in ((lambda: moe.grouped_mm(x, w, off, y, ws), y), (lambda: moe.grouped_mm_dx(dy, w, off, dx, ws), dx),
+                          (lambda: moe.grouped_mm_dw(dy, x, off, dw, ws), dw)):
+            call()
+            assert moe.read_device_error(ws) == 6, bad
+            assert bool((out == 7.0).all())
+    off = torch.tensor([0, 5, 5, 20], dtype=torch.int32, device=cuda_device)
+    y = torch.empty(20, 64, dtype=BF, device=cuda_device)
+    moe.grouped_mm(x, w, off, y, ws)
+    assert moe.read_device_error(ws) == 0 and bool((y == n_in).all())   # 127 and 128 are bf16 values
+
+
+def test_overlap_and_host_memory_refused(cuda_device, ws):
+    w = torch.zeros(1, 64, 64, dtype=BF, device=cuda_device)
+    x = torch.zeros(8, 64, dtype=BF, device=cuda_device)
+    with pytest.raises(moe.MoEError, match="overlaps x"):
+        moe.grouped_mm(x, w, None, x, ws)
+    with pytest.raises(moe.MoEError, match="overlaps w"):
+        moe.grouped_mm(x, w, None, w[0, :8], ws)
+    with pytest.raises(ValueError):
+        moe.grouped_mm(x.cpu(), w, None, x, ws)
+    with pytest.raises(moe.MoEError) as e:
+        moe.grouped_mm(x, w, None, torch.zeros_like(x), ws[:4096])
+    assert e.value.status == 3
+    s = torch.zeros(1, 8, device=cuda_device)
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.quant_fp8(x, x.view(-1).view(torch.uint8)[:512].view(8, 64), s)
+
+
+def test_streams_and_graphs(cuda_device):
+    """Two streams with a workspace each, and a captured call replayed on new inputs."""
+    g = gen(8, cuda_device)
+    counts = [2, 0, 30, 1]
+    off = offsets_of(counts, cuda_device)
+    w = normal(g, BF, 4, 256, 1024, std=0.05)
+    streams = [torch.cuda.Stream(cuda_device) for _ in range(2)]
+    spaces = [moe.alloc_grouped_workspace(cuda_device) for _ in range(2)]
+    xs = [normal(g, BF, 33, 1024) for _ in range(2)]
+    ys = [torch.zeros(33, 256, dtype=FP, device=cuda_device) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, sp, x, y in zip(streams, spaces, xs, ys):
+            moe.grouped_mm(x, w, off, y, sp, stream=s)
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        ref, mag = reference("mm", x, w, off, 4)
+        close(y, ref, mag, 1024)
+    graph = torch.cuda.CUDAGraph()
+    x, y = xs[0].clone(), torch.zeros_like(ys[0])
+    dy, dx, dw = normal(g, BF, 33, 256), torch.zeros(33, 1024, dtype=BF, device=cuda_device), torch.zeros_like(w)
+    with torch.cuda.graph(graph):
+        moe.grouped_mm(x, w, off, y, spaces[0])
+        moe.grouped_mm_dx(dy, w, off, dx, spaces[0])
+        moe.grouped_mm_dw(dy, x, off, dw, spaces[0])
+    for seed in range(3):
+        x.copy_(normal(gen(100 + seed, cuda_device), BF, 33, 1024))
+        graph.replay()
+        ref, mag = reference("mm", x, w, off, 4)
+        close(y, ref, mag, 1024)
+        ref, mag = reference("dx", dy, w, off, 4)
+        close(dx, ref, mag, 256)
+        ref, mag = reference("dw", dy, x, off, 4)
+        close(dw, ref, mag, 33)
+    new = torch.tensor([0, 10, 10, 11, 33], dtype=torch.int32, device=cuda_device)   # other row ranges, same graph
+    off.copy_(new)
+    graph.replay()
+    ref, mag = reference("mm", x, w, new, 4)
+    close(y, ref, mag, 1024)
+    assert [moe.read_device_error(s) for s in spaces] == [0, 0]
+
+
+def test_gradients_by_differences(cuda_device, ws):
+    """The loss is linear in x and in W, so a difference quotient along any direction is exact but for rounding."""
+    g = gen(21, cuda_device)
+    counts, n_in, n_out = [3, 0, 18, 7], 96, 80
+    off = offsets_of(counts, cuda_device)
+    x, w = normal(g, HF, 28, n_in), normal(g, HF, 4, n_out, n_in, std=0.1)
+    dy = normal(g, HF, 28, n_out)
+
+    def loss(x_, w_):
+        y = torch.empty(28, n_out, dtype=FP, device=cuda_device)
+        moe.grouped_mm(x_, w_, off, y, ws)
+        return (y.double() * dy.double()).sum()
+
+    dx, dw = torch.empty(28, n_in, dtype=FP, device=cuda_device), torch.empty(4, n_out, n_in, dtype=FP, device=cuda_device)
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    # directions of +-1/4 on values rounded to multiples of 2^-6: sums with them are exact in fp16
+    x, w = (x * 64).round() / 64, (w * 64).round() / 64
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    size = reference("mm", x.abs() + 0.25, w.abs() + 0.25, off, 4)[1]
+    tol = 2 * (n_in + n_out + 40) * 2.0 ** -23 * float((size * dy.double().abs()).sum())
+    for _ in range(3):
+        v = torch.randint(0, 2, x.shape, generator=g, device=cuda_device).to(HF) * 0.5 - 0.25
+        assert abs(float(loss(x + v, w) - loss(x, w) - (dx.double() * v.double()).sum())) <= tol
+        v = torch.randint(0, 2, w.shape, generator=g, device=cuda_device).to(HF) * 0.5 - 0.25
+        assert abs(float(loss(x, w + v) - loss(x, w) - (dw.double() * v.double()).sum())) <= tol
+
+
+# ------------------------------------------------------------------ 8 bits
+def quant_reference(x):
+    """Codes and scales by the formula, each step rounded once to fp32."""
+    rows, n = x.shape
+    groups = (n + 127) // 128
+    v = torch.zeros(rows, groups * 128, dtype=FP, device=x.device)
+    v[:, :n] = x.float()
+    v = v.view(rows, groups, 128)
+    a = v.abs().amax(2).clamp(min=448 * 2.0 ** -126)
+    top = torch.full_like(a, 448.0)
+    codes = (v * (top / a)[:, :, None]).to(torch.float8_e4m3fn).view(rows, -1)[:, :n].contiguous()
+    return codes, (a / top).t().contiguous()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows,n,ld_pad,shift", [(1, 4096, 0, 0), (1, 1, 0, 0), (37, 1024, 0, 0), (5, 128, 8, 0),
+                                                 (33, 144, 0, 0), (64, 100, 0, 0), (70, 513, 3, 1), (3, 2048, 0, 1),
+                                                 (300, 16, 16, 8), (2, 1000, 0, 0)])
+def test_quant(cuda_device, dtype, rows, n, ld_pad, shift):
+    g = gen(rows + n, cuda_device)
+    x = strided(g, dtype, rows, n, ld_pad, shift)
+    x[0, : n // 2] = 0
+    codes = torch.zeros(rows, n, dtype=torch.float8_e4m3fn, device=cuda_device)
+    scales = torch.zeros((n + 127) // 128, rows, device=cuda_device)
+    moe.quant_fp8(x, codes, scales)
+    ref, s = quant_reference(x)
+    assert torch.equal(scales, s)
+    assert torch.equal(codes.view(torch.uint8), ref.view(torch.uint8))
+    # half a step of the code, relative to the value: 2^-4, or 2^-10 of the scale among e4m3's subnormals;
+    # the two fp32 roundings of the factor and product move a value by 2^-23 at most
+    full = s.t().repeat_interleave(128, 1)[:, :n].double()
+    err = (codes.double() * full - x.double()).abs()
+    assert bool((err <= (2.0 ** -4 * (1 + 2.0 ** -10)) * x.double().abs() + 2.0 ** -10 * full * (1 + 2.0 ** -10)).all())
+
+
+def test_quant_extremes(cuda_device):
+    """Zeros, the smallest and largest values, and groups with an infinity or a NaN."""
+    x = torch.zeros(8, 256, dtype=BF, device=cuda_device)
+    x[1, 3] = 2.0 ** -133                       # a bf16 subnormal
+    x[2, 130] = torch.finfo(BF).max
+    x[2, 131] = -torch.finfo(BF).max
+    x[3] = torch.linspace(-3, 3, 256).to(BF)
+    x[4, 5], x[5, 200], x[6, 128] = float("inf"), float("nan"), float("-inf")
+    x[4, 6] = 1.0
+    for strip in (False, True):                 # 16-byte aligned rows, and odd ones
+        v = x[:, 1:] if strip else x
+        codes = torch.zeros(v.shape, dtype=torch.float8_e4m3fn, device=cuda_device)
+        scales = torch.zeros(2, 8, device=cuda_device)
+        moe.quant_fp8(v, codes, scales)
+        ref, s = quant_reference(v)
+        assert torch.equal(torch.isnan(scales), torch.isnan(s)) and torch.equal(scales.nan_to_num(1.0), s.nan_to_num(1.0))
+        assert torch.equal(codes.float().nan_to_num(99.0), ref.float().nan_to_num(99.0))
+        value = codes.float() * scales.t().repeat_interleave(128, 1)[:, :v.shape[1]]
+        assert bool(torch.isnan(value[4, :128]).all()) and bool((value[4, 128:] == 0).all())
+        assert bool(torch.isnan(value[5, 128:]).all()) and bool((value[5, :128] == 0).all())
+        assert bool((value[0] == 0).all()) and bool(torch.isfinite(value[1:4]).all())
+
+
+def fp8_inputs(g, experts, rows, n_in, n_out, ld_pad=0, shift=0):
+    dev = g.device
+    codes = torch.empty(rows * (n_in + ld_pad) + shift, dtype=torch.uint8, device=dev)
+    codes = codes[shift:].view(rows, n_in + ld_pad)[:, :n_in]
+    v = normal(g, FP, rows, n_in, std=100.0).clamp(-448, 448).to(torch.float8_e4m3fn)
+    codes.copy_(v.view(torch.uint8))
+    w = torch.empty(experts * n_out * n_in + shift, dtype=torch.uint8, device=dev)[shift:].view(experts, n_out, n_in)
+    w.copy_(normal(g, FP, experts, n_out, n_in, std=100.0).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    gi, go = (n_in + 127) // 128, (n_out + 127) // 128
+    sx = torch.exp(normal(g, FP, gi, rows, std=2.0)) * 0.01
+    sw = torch.exp(normal(g, FP, experts, go, gi, std=2.0)) * 0.001
+    return codes, sx, w, sw
+
+
+def fp8_wide(codes, s, n_out=None):
+    """Values of 8-bit rows ([groups, rows] scales) or weights (block scales) in 64 bits."""
+    v = codes.view(torch.float8_e4m3fn).double() if codes.is_contiguous() else \
+        codes.contiguous().view(torch.float8_e4m3fn).double()
+    if v.dim() == 2:
+        return v * s.t().repeat_interleave(128, 1)[:, :v.shape[1]].double()
+    return v * s.repeat_interleave(128, 1)[:, :v.shape[1]].repeat_interleave(128, 2)[:, :, :v.shape[2]].double()
+
+
+def run_fp8(counts, n_in, n_out, out, dev, ws, pad=0, ld_pad=0, shift=0, dense=False):
+    g = gen(n_in + n_out, dev)
+    experts, rows = len(counts), int(sum(counts)) + pad
+    off = None if dense else offsets_of(counts, dev)
+    codes, sx, w, sw = fp8_inputs(g, experts, rows, n_in, n_out, ld_pad, shift)
+    y = torch.full((rows, n_out + ld_pad), 7.0, dtype=out, device=dev)[:, :n_out]
+    moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    ref, mag = reference("mm", fp8_wide(codes, sx), fp8_wide(w, sw), off, experts)
+    used = rows - pad
+    close(y[:used], ref[:used], mag[:used], n_in, ("fp8", counts, n_in, n_out))
+    assert bool((y[used:] == 7.0).all())
+    return y
+
+
+@pytest.mark.parametrize("out", [BF, FP])
+@pytest.mark.parametrize("n_in,n_out", [(256, 128), (128, 320), (144, 40), (16, 8), (640, 264), (1, 1), (100, 129),
+                                        (300, 257)])
+def test_fp8_ragged(cuda_device, ws, out, n_in, n_out):
+    run_fp8(RAGGED, n_in, n_out, out, cuda_device, ws)
+
+
+@pytest.mark.parametrize("counts", [[1], [0, 0], [256], [300, 0, 513], [1] * 300, [16] * 40])
+def test_fp8_row_counts(cuda_device, ws, counts):
+    run_fp8(counts, 384, 256, FP, cuda_device, ws, pad=3)
+
+
+@pytest.mark.parametrize("ld_pad,shift", [(16, 0), (48, 16), (3, 0), (0, 1), (16, 5)])
+def test_fp8_strides_and_alignment(cuda_device, ws, ld_pad, shift):
+    run_fp8([5, 0, 70, 33], 256, 192, torch.float16 if shift == 5 else BF, cuda_device, ws, ld_pad=ld_pad, shift=shift)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 33, 300])
+def test_fp8_one_matrix(cuda_device, ws, rows):
+    a = run_fp8([rows], 4096, 320, FP, cuda_device, ws, dense=True)
+    assert torch.equal(a, run_fp8([rows], 4096, 320, FP, cuda_device, ws, dense=True))
+
+
+def test_fp8_nan_stays_in_its_row(cuda_device, ws):
+    g = gen(5, cuda_device)
+    counts = [4, 30]
+    off = offsets_of(counts, cuda_device)
+    codes, sx, w, sw = fp8_inputs(g, 2, 40, 256, 136)
+    ref, mag = reference("mm", fp8_wide(codes, sx), fp8_wide(w, sw), off, 2)
+    codes[7, 3] = 0x7F
+    sx[1, 9] = float("nan")
+    codes[34:] = 0x7F
+    sx[:, 34:] = float("nan")
+    y = torch.zeros(40, 136, dtype=FP, device=cuda_device)
+    moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
+    keep = [r for r in range(34) if r not in (7, 9)]
+    close(y[keep], ref[keep], mag[keep], 256)
+    assert bool(torch.isnan(y[[7, 9]]).all()) and bool((y[34:] == 0).all())
+
+
+# ----------------------------------------------------------- used together
+def _routed(dev, T, d, E, k, seed):
+    g = gen(seed, dev)
+    dims = moe.make_dims(T, d, 128, E, k)
+    wsl = moe.alloc_workspace(dims, dev)
+    x = normal(g, BF, T, d)
+    rw, rb = normal(g, FP, E, d, std=0.05), normal(g, FP, E, std=0.1)
+    ids, wt = torch.empty(T, k, dtype=torch.int32, device=dev), torch.empty(T, k, device=dev)
+    off = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    srt, inv = torch.empty(T * k, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev)
+    moe.route(dims, x, rw, rb, None, None, ids, wt, wsl)
+    moe.permute(dims, ids, off, srt, inv, wsl)
+    assert moe.read_device_error(wsl) == 0
+    return g, dims, wsl, x, ids, wt, off, srt, inv
+
+
+@pytest.mark.parametrize("T", [1, 45])
+def test_layer_over_source_weights(cuda_device, ws, T):
+    """route, permute, three 16-bit products with SwiGLU between them, combine: the layer before its weights are
+    packed, against the same sums in 64 bits (intermediate rounding to bf16 included, so 2^-8 of each stage)."""
+    d, f, E, k = 256, 128, 8, 3
+    g, dims, wsl, x, ids, wt, off, srt, inv = _routed(cuda_device, T, d, E, k, 31)
+    w1, w3 = normal(g, BF, E, f, d, std=0.05), normal(g, BF, E, f, d, std=0.05)
+    w2 = normal(g, BF, E, d, f, std=0.05)
+    xs = x[(srt // k).long()]
+    h1, h3 = (torch.empty(T * k, f, dtype=FP, device=cuda_device) for _ in range(2))
+    y = torch.empty(T * k, d, dtype=FP, device=cuda_device)
+    moe.grouped_mm(xs, w1, off, h1, ws)
+    moe.grouped_mm(xs, w3, off, h3, ws)
+    h = (torch.nn.functional.silu(h1) * h3).to(BF)
+    moe.grouped_mm(h, w2, off, y, ws)
+    out = torch.empty(T, d, dtype=BF, device=cuda_device)
+    moe.combine(dims, y, inv, wt, None, out)
+    assert moe.read_device_error(ws) == 0
+    ref, mag = torch.zeros(T, d, dtype=torch.float64, device=cuda_device), 0
+    mag = torch.zeros_like(ref)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            a, b = w1[e].double() @ x[t].double(), w3[e].double() @ x[t].double()
+            hh = torch.nn.functional.silu(a) * b
+            ref[t] += float(wt[t, j]) * (w2[e].double() @ hh)
+            mag[t] += float(wt[t, j]) * (w2[e].double().abs() @ hh.abs())
+    # h is rounded to bf16 (2^-8 of each term, plus fp32 sums of 256 terms well below it), the output once more
+    assert bool(((out.double() - ref).abs() <= 2.0 ** -8 * 1.05 * mag + 2.0 ** -8 * ref.abs() + 1e-6).all())
+
+
+def test_layer_over_8bit_weights(cuda_device, ws):
+    """The gate projection of routed rows, quantised to 8 bits, over 8-bit weights."""
+    T, d, E, k, f = 45, 256, 8, 3, 192
+    g, dims, wsl, x, ids, wt, off, srt, inv = _routed(cuda_device, T, d, E, k, 32)
+    _, _, w, sw = fp8_inputs(g, E, 1, d, f)
+    xs = x[(srt // k).long()]
+    codes = torch.empty(T * k, d, dtype=torch.float8_e4m3fn, device=cuda_device)
+    sx = torch.empty(d // 128, T * k, device=cuda_device)
+    moe.quant_fp8(xs, codes, sx)
+    y = torch.empty(T * k, f, dtype=BF, device=cuda_device)
+    moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
+    assert moe.read_device_error(ws) == 0
+    wide_w = fp8_wide(w, sw)
+    ref, mag = reference("mm", fp8_wide(codes, sx), wide_w, off, E)
+    close(y, ref, mag, d)
+    # against the rows before quantisation: half a code step (2^-4 of the value, 2^-10 of the scale) of each term
+    full, m = reference("mm", xs, wide_w, off, E)
+    step = reference("mm", sx.t().repeat_interleave(128, 1), wide_w, off, E)[1]
+    assert bool(((y.double() - full).abs() <= 2.0 ** -4 * 1.01 * m + 2.0 ** -10 * 1.01 * step +
+                 (d + 4) * 2.0 ** -23 * 2 * m + 2.0 ** -8 * 1.1 * full.abs() + 2.0 ** -12 * m).all())
+
+
+def test_training_step(cuda_device, ws):
+    """Forward, both gradients and a step against torch's own gradient of the same loss in 64 bits."""
+    g = gen(41, cuda_device)
+    counts, n_in, n_out = [12, 0, 33, 3], 128, 96
+    off = offsets_of(counts, cuda_device)
+    x, w, t = normal(g, BF, 48, n_in), normal(g, BF, 4, n_out, n_in, std=0.05), normal(g, FP, 48, n_out)
+    y = torch.empty(48, n_out, dtype=FP, device=cuda_device)
+    moe.grouped_mm(x, w, off, y, ws)
+    dy = (y - t).to(BF)
+    dx, dw = torch.empty_like(x), torch.empty(4, n_out, n_in, dtype=FP, device=cuda_device)
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+    o = off.tolist()
+    y64 = torch.cat([x64[o[e]:o[e + 1]] @ w64[e].t() for e in range(4)])
+    (y64 * dy.double()).sum().backward()
+    _, mag = reference("dx", dy, w, off, 4)
+    close(dx, x64.grad, mag, n_out)
+    _, mag = reference("dw", dy, x, off, 4)
+    close(dw, w64.grad, mag, 48)
+    assert moe.read_device_error(ws) == 0
