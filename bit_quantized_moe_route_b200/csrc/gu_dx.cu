@@ -1,0 +1,5 @@
+// Grouped tensor-memory kernel: gradient of the rows.
+#define GU_OP G_DX
+#define GU_FP8 false
+#define GU_CHAIN 0
+#include "gu_inst.inl"

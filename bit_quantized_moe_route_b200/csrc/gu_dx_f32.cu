@@ -1,0 +1,5 @@
+// Grouped tensor-memory kernel: gradient of the rows, fp32 outputs.
+#define GU_OP G_DX
+#define GU_FP8 false
+#define GU_CHAIN kGuChain
+#include "gu_inst.inl"

@@ -1,0 +1,48 @@
+// Instantiation unit of the grouped tensor-memory kernel (GU_OP, GU_FP8,
+// GU_CHAIN set by the including file).
+#include "grouped_umma.cuh"
+
+namespace moe {
+
+namespace {
+cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kGuThreads);
+  cfg.dynamicSmemBytes = gu_smem();
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+}  // namespace
+
+template <>
+bool gu_launch<GU_OP, GU_FP8, GU_CHAIN>(const GuParams& p, int pairs, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
+  return cudaLaunchKernelEx(&cfg, grouped_umma_kernel<GU_OP, GU_FP8, GU_CHAIN>, p) == cudaSuccess;
+}
+
+template <>
+int gu_pairs<GU_OP, GU_FP8, GU_CHAIN>() {
+  if (cudaFuncSetAttribute(grouped_umma_kernel<GU_OP, GU_FP8, GU_CHAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)gu_smem()) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_umma_kernel<GU_OP, GU_FP8, GU_CHAIN>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n < kGuPairsMax ? n : kGuPairsMax;
+}
+
+}  // namespace moe
