@@ -20,8 +20,14 @@
 // comes from beyond the tensor's end, which TMA fills with zeros, so that no
 // value of another expert's rows (a NaN, say) enters a product.
 //
-// Work is split by steps, not by tiles: all steps of all tiles are one line,
-// cut into equal pieces, one per pair of CTAs.  A tile that a cut goes through
+// Work is split by steps, not by tiles.  The tiles, in the order expert, M
+// tile, row tile, are dealt out to the pairs of CTAs in turn, so that pairs
+// that run at the same time read the same weights and rows from L2 (with
+// each pair on a run of neighbouring tiles instead, 74 pairs stream 148 MB
+// between two uses of an operand tile, more than L2 holds: 32,768 rows over 32
+// experts took 870 us that way).  The pairs' hands, one after the other, are a
+// line, and the line is cut into pieces of equal cost, one per pair.  A tile
+// that a cut goes through
 // is summed by the pairs that hold parts of it: each writes its fp32 partial
 // sums to the workspace and counts itself in; the last one adds the partials
 // in the pieces' order (so the result does not depend on who was last) and
@@ -65,11 +71,6 @@ struct alignas(64) GuParams {
   int split_most;        // pieces that a tile may be cut into
   unsigned char* ws;
 };
-
-constexpr size_t gu_smem() {
-  return 1024 + (size_t)kGuStages * 2 * kGuTile + kGuScaleSlots * kGuN * 4 + (kGmmMaxExperts + 1) * 8 + 512;
-}
-static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
 // ------------------------------------------------------------ PTX wrappers
 MOE_DEV void gu_tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -126,59 +127,87 @@ MOE_DEV void gu_ld32(uint32_t taddr, float (&v)[32]) {
 struct GuItem {
   int e, m0, n0, nv, np;   // expert, first M value, first output row (dw: first o), rows in use, MMA width
   int kb0, kb1, nkb;       // steps, and the tile's number of steps
+  int cost;                // of one step
   int r0, r1;              // dw: the expert's rows
-  bool none;               // dw: no rows; one unit without steps, zeros to write
-  long long tile0;         // the tile's first unit on the line of steps
+  bool none;               // dw: no rows; one step that reads nothing, zeros to write
+  long long pos;           // where the tile begins on the line
 };
 
-template <int OP>
+// The line of work and this pair's piece of it (shared memory of each CTA).
+struct GuLine {
+  long long col[kGuPairsMax + 1];  // where each pair's hand begins
+  long long cost_most;             // of a step
+  long long start_pos;             // the piece's first tile: where it begins, whose hand, which of it
+  int start_col, start_row;
+  int flag;
+};
+
+constexpr size_t gu_smem() {
+  return 1024 + (size_t)kGuStages * 2 * kGuTile + kGuScaleSlots * kGuN * 4 + (kGmmMaxExperts + 1) * 8 +
+         sizeof(GuLine) + 512;
+}
+static_assert(gu_smem() <= 227 * 1024, "shared memory");
+
+template <int OP, int KE>
+struct GuTiles {
+  // (dw: whole 64-value panels in both CTAs)
+  static constexpr int kRound = OP == G_DW ? 128 : 32;
+  MOE_DEV static int count(int n) { return (n + kGuN - 1) / kGuN; }
+  MOE_DEV static int m_count(const GmmProblem& p) { return ((OP == G_MM ? p.n_out : p.n_in) + 255) >> 8; }
+  MOE_DEV static int of_expert(const GmmProblem& p, int rows) {
+    return m_count(p) * count(OP == G_DW ? p.n_out : rows);
+  }
+  MOE_DEV static int steps(const GmmProblem& p, int rows) {
+    return OP == G_MM ? (p.n_in + KE - 1) / KE : OP == G_DX ? (p.n_out + KE - 1) / KE : max(1, (rows + KE - 1) / KE);
+  }
+  // Tile g whole: an expert's rows are cut into equal tiles.  A step's cost
+  // is its operands' bytes (256 rows of A, np of B), between that of reading
+  // weights from HBM (the same for every np) and that of the MMA.
+  MOE_DEV static void get(const GmmProblem& p, const long long* cum, int g, GuItem& it) {
+    it.e = gmm_expert_of(cum, p.E, g);
+    it.r0 = gmm_off(p, it.e);
+    it.r1 = gmm_off(p, it.e + 1);
+    const int n_all = OP == G_DW ? p.n_out : it.r1 - it.r0;
+    const unsigned nt = (unsigned)count(n_all), tile = (unsigned)(g - cum[it.e]);
+    const int tn = min(kGuN, (int)(((unsigned)n_all + nt - 1) / nt + kRound - 1) & ~(kRound - 1));
+    const int t_m = (int)(tile / nt), n_begin = (int)(tile % nt) * tn;
+    it.m0 = t_m * 256;
+    it.nv = max(0, min(tn, n_all - n_begin));
+    it.np = max(kRound, (it.nv + kRound - 1) & ~(kRound - 1));
+    it.n0 = OP == G_DW ? n_begin : it.r0 + n_begin;
+    it.nkb = steps(p, it.r1 - it.r0);
+    it.none = OP == G_DW && it.r1 == it.r0;
+    it.cost = 256 + it.np;
+  }
+};
+
+// Walks a piece; every warp that does, and both CTAs of the pair, see the same items.
+template <int OP, int KE>
 struct GuWalk {
   const GmmProblem& p;
   const long long* cum;
-  int m_tiles, k_elems, e;
-  long long cur, end;
+  int col, row, cols, n_tiles;
+  long long pos, begin, end;
 
-  MOE_DEV GuWalk(const GmmProblem& p_, const long long* cum_, int k_elems_, long long begin, long long end_)
-      : p(p_), cum(cum_), k_elems(k_elems_), cur(begin), end(end_) {
-    m_tiles = ((OP == G_MM ? p.n_out : p.n_in) + 255) >> 8;
-    e = begin < end_ ? gmm_expert_of(cum, p.E, begin) : 0;
-  }
-  // tiles along N and rows per tile of a range of n
-  MOE_DEV static int tiles(int n) { return (n + kGuN - 1) / kGuN; }
-  // (dw: whole 64-value panels in both CTAs)
-  static constexpr int kRound = OP == G_DW ? 128 : 32;
-  MOE_DEV static int per_tile(int n, int nt) {
-    return min(kGuN, ((n + nt - 1) / nt + kRound - 1) & ~(kRound - 1));
-  }
-  MOE_DEV static int steps(const GmmProblem& p, int k_elems, int rows) {
-    return OP == G_MM ? (p.n_in + k_elems - 1) / k_elems
-           : OP == G_DX ? (p.n_out + k_elems - 1) / k_elems
-                        : max(1, (rows + k_elems - 1) / k_elems);
-  }
+  MOE_DEV GuWalk(const GmmProblem& p_, const long long* cum_, const GuLine& line, int cols_, long long begin_,
+                 long long end_)
+      : p(p_), cum(cum_), col(line.start_col), row(line.start_row), cols(cols_), n_tiles((int)cum_[p_.E]),
+        pos(line.start_pos), begin(begin_), end(end_) {}
   MOE_DEV bool next(GuItem& it) {
-    if (cur >= end) return false;
-    while (cum[e + 1] <= cur) ++e;
-    it.e = e;
-    it.r0 = gmm_off(p, e);
-    it.r1 = gmm_off(p, e + 1);
-    const int n_all = OP == G_DW ? p.n_out : it.r1 - it.r0;
-    const int nt = tiles(n_all), tn = per_tile(n_all, nt);
-    it.nkb = steps(p, k_elems, it.r1 - it.r0);
-    const long long local = cur - cum[e];
-    // an expert's units fit 32 bits (its tiles times its steps; refused by the host otherwise)
-    const unsigned tile = (unsigned)local / (unsigned)it.nkb;
-    it.kb0 = (int)((unsigned)local - tile * (unsigned)it.nkb);
-    it.kb1 = (int)min((long long)it.nkb, it.kb0 + (end - cur));
-    const int t_n = (int)(tile % (unsigned)nt), t_m = (int)(tile / (unsigned)nt);
-    it.m0 = t_m * 256;
-    const int n_begin = t_n * tn;
-    it.nv = min(tn, n_all - n_begin);
-    it.np = (it.nv + kRound - 1) & ~(kRound - 1);
-    it.n0 = OP == G_DW ? n_begin : it.r0 + n_begin;
-    it.none = OP == G_DW && it.r1 == it.r0;
-    it.tile0 = cur - it.kb0;
-    cur += it.kb1 - it.kb0;
-    return true;
+    while (pos < end) {
+      GuTiles<OP, KE>::get(p, cum, row * cols + col, it);
+      it.pos = pos;
+      it.kb0 = pos >= begin ? 0 : (int)((begin - pos + it.cost - 1) / it.cost);
+      const long long to = (end - pos + it.cost - 1) / it.cost;
+      it.kb1 = to < it.nkb ? (int)to : it.nkb;
+      pos += (long long)it.nkb * it.cost;
+      if (++row * (long long)cols + col >= n_tiles) {
+        row = 0;
+        ++col;
+      }
+      if (it.kb0 < it.kb1) return true;
+    }
+    return false;
   }
 };
 
@@ -216,9 +245,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   const uint32_t base = (raw32 + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - raw32);
   constexpr uint32_t kScaleOff = kGuStages * 2 * kGuTile, kCumOff = kScaleOff + kGuScaleSlots * kGuN * 4,
-                     kBarOff = kCumOff + (kGmmMaxExperts + 1) * 8 + 8;
-  const uint32_t sc0 = base + kScaleOff, bar = (base + kBarOff + 7u) & ~7u;
+                     kLineOff = kCumOff + (kGmmMaxExperts + 1) * 8, kBarOff = kLineOff + sizeof(GuLine);
+  const uint32_t sc0 = base + kScaleOff, bar = base + kBarOff;
   long long* cum = reinterpret_cast<long long*>(gen + kCumOff);
+  GuLine& line = *reinterpret_cast<GuLine*>(gen + kLineOff);
   // (L): used in the leader CTA only
   auto full = [&](int s) { return bar + 8u * s; };                                   // (L) TMA bytes of both CTAs
   auto empty = [&](int s) { return bar + 8u * (kGuStages + s); };                    // MMA commit
@@ -232,8 +262,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   int* tail = reinterpret_cast<int*>(gen + (bar - base) + 8 * (kBars + 2));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = tail + 1;
-  int* flag = tail + 2;
-  int* last_flag = tail + 3;
+  int* last_flag = tail + 2;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, pair, npairs;
@@ -267,39 +296,97 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  using Tiles = GuTiles<OP, KE>;
+  using Walk = GuWalk<OP, KE>;
   const int m_all = OP == G_MM ? g.n_out : g.n_in;
-  const int m_tiles = (m_all + 255) >> 8;
+  const int cols = (int)npairs;
   const bool plan_ok = gmm_plan(
-      g,
-      [&](int rows) -> long long {
-        const int nt = GuWalk<OP>::tiles(OP == G_DW ? g.n_out : rows);
-        return (long long)m_tiles * nt * GuWalk<OP>::steps(g, KE, rows);
-      },
-      cum, flag);
-  tc_fence_before();
-  cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated before any cross-CTA use
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  // This pair's piece of the line of steps.  Both CTAs of a pair and every
-  // warp derive the same piece and items from the same numbers.
-  const long long total = plan_ok ? cum[g.E] : 0;
-  long long pieces = npairs < total ? npairs : total;
-  {
-    long long tiles_all;
-    if constexpr (OP == G_DW) tiles_all = (long long)g.E * m_tiles * GuWalk<OP>::tiles(g.n_out);
-    else tiles_all = total / GuWalk<OP>::steps(g, KE, 0);
-    if (pieces > tiles_all * p.split_most) pieces = tiles_all * p.split_most;
+      g, [&](int rows) -> long long { return Tiles::of_expert(g, rows); }, cum, &line.flag);
+  const int n_tiles = plan_ok ? (int)cum[g.E] : 0;
+  for (int i = tid; i <= cols; i += kGuThreads) line.col[i] = 0;
+  if (tid == 0) {
+    line.cost_most = 0;
+    line.start_pos = 0;
+    line.start_col = line.start_row = 0;
+  }
+  __syncthreads();
+  for (int t = tid; t < n_tiles; t += kGuThreads) {  // the cost of each hand
+    GuItem it;
+    Tiles::get(g, cum, t, it);
+    atomicAdd(reinterpret_cast<unsigned long long*>(&line.col[t % cols]), (unsigned long long)it.nkb * it.cost);
+    atomicMax(reinterpret_cast<unsigned long long*>(&line.cost_most), (unsigned long long)it.cost);
+  }
+  __syncthreads();
+  if (warp == 0) {  // hands one after the other
+    long long sum = 0;
+    for (int c0 = 0; c0 < cols; c0 += 32) {
+      const long long v = c0 + lane < cols ? line.col[c0 + lane] : 0;
+      long long x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (c0 + lane < cols) line.col[c0 + lane] = sum + x - v;
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) line.col[cols] = sum;
+  }
+  __syncthreads();
+  // Pieces: one per pair, none shorter than a step (each piece that a tile
+  // reaches into then holds a step of it), a tile cut into split_most at most.
+  const long long total = line.col[cols];
+  long long pieces = 0;
+  if (total > 0) {
+    pieces = min((long long)cols, total / line.cost_most);
+    pieces = min(pieces, (long long)n_tiles * p.split_most);
   }
   const long long begin = pair < pieces ? (long long)pair * total / pieces : 0;
   const long long end = pair < pieces ? ((long long)pair + 1) * total / pieces : 0;
   auto piece_of = [&](long long u) { return (int)(((u + 1) * pieces - 1) / total); };
+  if (warp == 0 && begin < end) {  // the piece's first tile
+    int c = 0;
+    for (int c0 = 0; c0 < cols; c0 += 32)
+      c += __popc(__ballot_sync(0xffffffffu, c0 + lane < cols && line.col[c0 + lane + 1] <= begin));
+    long long at = line.col[c];
+    for (int row = 0;; row += 32) {
+      const long long t = (long long)(row + lane) * cols + c;
+      long long w = 0;
+      if (t < n_tiles) {
+        GuItem it;
+        Tiles::get(g, cum, (int)t, it);
+        w = (long long)it.nkb * it.cost;
+      }
+      long long x = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, w > 0 && at + x > begin);
+      if (here) {
+        if (lane == __ffs(here) - 1) {
+          line.start_pos = at + x - w;
+          line.start_col = c;
+          line.start_row = row + lane;
+        }
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, x, 31);
+      if ((long long)(row + 32) * cols + c >= n_tiles) break;  // not reached: begin lies in this hand
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated before any cross-CTA use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     // ================= TMA issuer of this CTA's halves of both operands
     if (lane == 0) {
       um_prefetch_map(&p.a_map);
-      GuWalk<OP> walk(g, cum, KE, begin, end);
+      Walk walk(g, cum, line, cols, begin, end);
       GuItem it;
       int st = 0;
       uint32_t ph = 0;
@@ -362,7 +449,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   } else if (warp == 1) {
     // ================= MMA issuer (leader CTA)
     if (leader && lane == 0) {
-      GuWalk<OP> walk(g, cum, KE, begin, end);
+      Walk walk(g, cum, line, cols, begin, end);
       GuItem it;
       int st = 0, seg = 0;
       uint32_t ph = 0;
@@ -417,7 +504,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   } else if (warp == 2) {
     // ================= 8-bit product: the scales of each step, row scale times this CTA's weight scale
     if constexpr (FP8) {
-      GuWalk<OP> walk(g, cum, KE, begin, end);
+      Walk walk(g, cum, line, cols, begin, end);
       GuItem it;
       int slot = 0;
       uint32_t ph = 0;
@@ -463,7 +550,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   } else if (warp >= 4) {
     // ================= epilogue: 32 TMEM lanes (M values) and every other 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
-    GuWalk<OP> walk(g, cum, KE, begin, end);
+    Walk walk(g, cum, line, cols, begin, end);
     GuItem it;
     int seg = 0, slot = 0;
     uint32_t sph = 0, jph = 0;
@@ -571,7 +658,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       }
       if (!whole) {
         // count this part in; the last part's CTA adds them all, in the pieces' order
-        const int first = piece_of(it.tile0), last = piece_of(it.tile0 + it.nkb - 1);
+        const int first = piece_of(it.pos), last = piece_of(it.pos + (long long)(it.nkb - 1) * it.cost);
         __threadfence();
         ok = epi_sync();
         if (!ok) break;
