@@ -20,20 +20,24 @@
 // comes from beyond the tensor's end, which TMA fills with zeros, so that no
 // value of another expert's rows (a NaN, say) enters a product.
 //
-// Work is split by steps, not by tiles.  The tiles, in the order expert, M
-// tile, row tile, are dealt out to the pairs of CTAs in turn, so that pairs
-// that run at the same time read the same weights and rows from L2 (with
-// each pair on a run of neighbouring tiles instead, 74 pairs stream 148 MB
-// between two uses of an operand tile, more than L2 holds: 32,768 rows over 32
-// experts took 870 us that way).  The pairs' hands, one after the other, are a
-// line, and the line is cut into pieces of equal cost, one per pair.  A tile
-// that a cut goes through
-// is summed by the pairs that hold parts of it: each writes its fp32 partial
-// sums to the workspace and counts itself in; the last one adds the partials
-// in the pieces' order (so the result does not depend on who was last) and
-// writes the outputs.  No pair waits for another.  This keeps every SM busy
-// when there are few tiles (one token over eight experts: 64 tiles for 74
-// pairs), and costs at most two partial tiles per pair.
+// The tiles, in the order expert, M tile, row tile, are dealt out to the pairs
+// of CTAs in turn, so that pairs that run at the same time read the same
+// weights and rows from L2 (with each pair on a run of neighbouring tiles
+// instead, 74 pairs stream 148 MB between two uses of an operand tile, more
+// than L2 holds: 32,768 rows over 32 experts took 870 us that way, 588 dealt
+// out).  All but the last one to two tiles per pair are dealt whole.  Those
+// last ones are split by steps: their steps are one line, cut so that every
+// pair has the same cost in all.  A tile that a cut goes through is summed by
+// the pairs that hold parts of it: each writes its fp32 partial sums to the
+// workspace and counts itself in; the last one adds the partials in the
+// pieces' order (so the result does not depend on who was last) and writes
+// the outputs.  No pair waits for another.  This keeps every SM busy when
+// there are few tiles (one token over eight experts: 64 tiles for 74 pairs),
+// and costs at most two partial tiles per pair.
+//
+// Tensor memory is a ring of eight slots of 64 columns; a sum takes one, two
+// or four of them, so that narrow tiles have up to eight sums in flight
+// between the MMA and the epilogue.
 //
 // CHAIN = 0: the tile's whole sum is taken in tensor memory.  CHAIN > 0: every
 // CHAIN steps the sum is handed to the epilogue warps, which add it to sums in
@@ -52,7 +56,12 @@ constexpr int kGuTile = 16384;            // bytes of one operand of one step
 constexpr int kGuN = 256;                 // output rows per tile
 constexpr int kGuThreads = 384;           // warps: 0 loads, 1 MMA, 2 scales, 4-11 epilogue
 constexpr int kGuEpiWarps = 8;
+constexpr int kGuRegs = 168;              // registers per thread at launch
+constexpr int kGuRegsLow = 88, kGuRegsHigh = 208;  // CHAIN > 0: warps 0-3, epilogue warps
+static_assert(128 * kGuRegsLow + 256 * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
 constexpr int kGuScaleSlots = 8;
+constexpr int kGuSegs = 8;                // sums between the MMA and the epilogue; TMEM slots
+constexpr int kGuSlotCols = 512 / kGuSegs;
 constexpr int kGuPart = 128 * kGuN * 4;   // bytes of one partial tile of one CTA
 constexpr int kGuPairsMax = 74;
 constexpr long long kGuLinger = 4000000;  // ~2 ms
@@ -122,6 +131,25 @@ MOE_DEV void gu_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// two fp32 in one register pair, and the packed instructions on them
+MOE_DEV unsigned long long gu_pack(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV void gu_unpack(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+MOE_DEV void gu_fma2(unsigned long long& c, unsigned long long a, unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
+MOE_DEV ulonglong2 gu_lds_u64x2(uint32_t a) {
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
+  return v;
+}
+
 // ------------------------------------------------------------ work items
 // A run of steps of one tile.
 struct GuItem {
@@ -133,19 +161,23 @@ struct GuItem {
   long long pos;           // where the tile begins on the line
 };
 
-// The line of work and this pair's piece of it (shared memory of each CTA).
+constexpr int kGuTailMost = 2 * kGuPairsMax;
+
+// The plan of a launch (shared memory of each CTA; the same in all of them).
 struct GuLine {
-  long long col[kGuPairsMax + 1];  // where each pair's hand begins
-  long long cost_most;             // of a step
-  long long start_pos;             // the piece's first tile: where it begins, whose hand, which of it
-  int start_col, start_row;
-  int flag;
+  long long tail[kGuTailMost + 1];  // the tiles that are split: where each begins on the line of costs
+  long long cut[kGuPairsMax + 1];   // where each pair's piece of that line begins
+  long long hand[kGuPairsMax];      // cost of the tiles that each pair has whole
+  int off[kGmmMaxExperts + 1];      // the experts' rows
+  int cum[kGmmMaxExperts + 1];      // the experts' tiles
+  int chunk[kGmmMaxExperts / 32];
 };
 
-constexpr size_t gu_smem() {
-  return 1024 + (size_t)kGuStages * 2 * kGuTile + kGuScaleSlots * kGuN * 4 + (kGmmMaxExperts + 1) * 8 +
-         sizeof(GuLine) + 512;
-}
+// shared memory from the first 1024-byte boundary: operand ring, scales, plan, barriers
+constexpr uint32_t kGuScaleOff = kGuStages * 2 * kGuTile;
+constexpr uint32_t kGuLineOff = kGuScaleOff + kGuScaleSlots * kGuN * 4;
+constexpr uint32_t kGuBarOff = (kGuLineOff + sizeof(GuLine) + 7) / 8 * 8;
+constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
 template <int OP, int KE>
@@ -160,56 +192,219 @@ struct GuTiles {
   MOE_DEV static int steps(const GmmProblem& p, int rows) {
     return OP == G_MM ? (p.n_in + KE - 1) / KE : OP == G_DX ? (p.n_out + KE - 1) / KE : max(1, (rows + KE - 1) / KE);
   }
-  // Tile g whole: an expert's rows are cut into equal tiles.  A step's cost
-  // is its operands' bytes (256 rows of A, np of B), between that of reading
-  // weights from HBM (the same for every np) and that of the MMA.
-  MOE_DEV static void get(const GmmProblem& p, const long long* cum, int g, GuItem& it) {
-    it.e = gmm_expert_of(cum, p.E, g);
-    it.r0 = gmm_off(p, it.e);
-    it.r1 = gmm_off(p, it.e + 1);
+  // rows per tile: an expert's rows are cut into nt equal tiles
+  MOE_DEV static int width(int n_all, int nt) {
+    return min(kGuN, (int)(((unsigned)n_all + nt - 1) / (unsigned)nt + kRound - 1) & ~(kRound - 1));
+  }
+  MOE_DEV static int padded(int nv) { return max(kRound, (nv + kRound - 1) & ~(kRound - 1)); }
+  // A step's cost is its operands' bytes (256 rows of A, np of B), between
+  // that of reading weights from HBM (the same for every np) and that of the MMA.
+  MOE_DEV static int cost(int np) { return 256 + np; }
+  // tile g whole
+  MOE_DEV static void get(const GmmProblem& p, const GuLine& l, int g, GuItem& it) {
+    int lo = 0, hi = p.E;  // cum[lo] <= g < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (l.cum[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    it.e = lo;
+    it.r0 = l.off[lo];
+    it.r1 = l.off[lo + 1];
     const int n_all = OP == G_DW ? p.n_out : it.r1 - it.r0;
-    const unsigned nt = (unsigned)count(n_all), tile = (unsigned)(g - cum[it.e]);
-    const int tn = min(kGuN, (int)(((unsigned)n_all + nt - 1) / nt + kRound - 1) & ~(kRound - 1));
-    const int t_m = (int)(tile / nt), n_begin = (int)(tile % nt) * tn;
+    const unsigned nt = (unsigned)count(n_all), tile = (unsigned)(g - l.cum[lo]);
+    const int tn = width(n_all, (int)nt);
+    const int t_m = (int)(tile / nt), n_begin = (int)(tile - (unsigned)t_m * nt) * tn;
     it.m0 = t_m * 256;
     it.nv = max(0, min(tn, n_all - n_begin));
-    it.np = max(kRound, (it.nv + kRound - 1) & ~(kRound - 1));
+    it.np = padded(it.nv);
     it.n0 = OP == G_DW ? n_begin : it.r0 + n_begin;
     it.nkb = steps(p, it.r1 - it.r0);
     it.none = OP == G_DW && it.r1 == it.r0;
-    it.cost = 256 + it.np;
+    it.cost = cost(it.np);
   }
 };
 
-// Walks a piece; every warp that does, and both CTAs of the pair, see the same items.
+// TMEM slots of sums n wide, in a ring; the MMA and the epilogue walk it alike.
+struct GuRing {
+  int pos = 0, used = 0;
+  MOE_DEV int take(int np) {  // first slot; `used`: how many
+    used = np <= kGuSlotCols ? 1 : np <= 2 * kGuSlotCols ? 2 : 4;
+    const int at = ((pos + used - 1) & ~(used - 1)) & (kGuSegs - 1);
+    pos = at + used;
+    return at;
+  }
+};
+
+// Walks a pair's work; every warp that does, and both CTAs of the pair, see the same items.
 template <int OP, int KE>
 struct GuWalk {
   const GmmProblem& p;
-  const long long* cum;
-  int col, row, cols, n_tiles;
-  long long pos, begin, end;
+  const GuLine& l;
+  int pair, cols, n_tiles, whole;  // whole: tiles dealt whole to each pair
+  int row;
+  long long begin, end;
 
-  MOE_DEV GuWalk(const GmmProblem& p_, const long long* cum_, const GuLine& line, int cols_, long long begin_,
-                 long long end_)
-      : p(p_), cum(cum_), col(line.start_col), row(line.start_row), cols(cols_), n_tiles((int)cum_[p_.E]),
-        pos(line.start_pos), begin(begin_), end(end_) {}
+  MOE_DEV GuWalk(const GmmProblem& p_, const GuLine& l_, int pair_, int cols_, int n_tiles_, int whole_)
+      : p(p_), l(l_), pair(pair_), cols(cols_), n_tiles(n_tiles_), whole(whole_), row(0) {
+    begin = l.cut[pair];
+    end = l.cut[pair + 1];
+    if (whole == 0) seek();
+  }
+  // to the piece's first tile: the last one that begins at or before it
+  MOE_DEV void seek() {
+    if (begin == end) return;
+    int lo = 0, hi = n_tiles - whole * cols;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (l.tail[mid] <= begin) lo = mid;
+      else hi = mid;
+    }
+    row = whole + lo;
+  }
   MOE_DEV bool next(GuItem& it) {
-    while (pos < end) {
-      GuTiles<OP, KE>::get(p, cum, row * cols + col, it);
-      it.pos = pos;
-      it.kb0 = pos >= begin ? 0 : (int)((begin - pos + it.cost - 1) / it.cost);
-      const long long to = (end - pos + it.cost - 1) / it.cost;
-      it.kb1 = to < it.nkb ? (int)to : it.nkb;
-      pos += (long long)it.nkb * it.cost;
-      if (++row * (long long)cols + col >= n_tiles) {
-        row = 0;
-        ++col;
-      }
+    if (row < whole) {
+      GuTiles<OP, KE>::get(p, l, row * cols + pair, it);
+      it.kb0 = 0;
+      it.kb1 = it.nkb;
+      it.pos = 0;
+      if (++row == whole) seek();
+      return true;
+    }
+    while (begin < end) {
+      const int t = row - whole;
+      if (whole * cols + t >= n_tiles || l.tail[t] >= end) break;
+      ++row;
+      GuTiles<OP, KE>::get(p, l, whole * cols + t, it);
+      it.pos = l.tail[t];
+      it.kb0 = steps_before(begin, it);
+      it.kb1 = steps_before(end, it);
       if (it.kb0 < it.kb1) return true;
     }
     return false;
   }
+  // steps of the tile that begin before `at`
+  MOE_DEV static int steps_before(long long at, const GuItem& it) {
+    const long long d = at - it.pos;
+    if (d <= 0) return 0;
+    if (d > (long long)(it.nkb - 1) * it.cost) return it.nkb;
+    return d < (1LL << 31) ? (int)(((unsigned)d + it.cost - 1) / (unsigned)it.cost) : (int)((d + it.cost - 1) / it.cost);
+  }
 };
+
+// Fills the plan; called by all threads.  Returns the number of tiles, -1 when
+// the offsets are not valid (they are the caller's, and checked before any is
+// used as an index: 0 <= off[0] <= ... <= off[E] <= rows).
+template <int OP, int KE>
+MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, int* whole_out) {
+  using Tiles = GuTiles<OP, KE>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarps = kGuThreads / 32;
+  for (int e = tid; e <= p.E; e += kGuThreads) l.off[e] = gmm_off(p, e);
+  __syncthreads();
+  int bad = 0;
+  const int chunks = (p.E + 31) >> 5;
+  for (int k = warp; k < chunks; k += kWarps) {
+    const int e = 32 * k + lane;
+    int n = 0;
+    if (e < p.E) {
+      const int a = l.off[e], b = l.off[e + 1];
+      if (a < 0 || b < a || b > p.rows) bad = 1;
+      else n = Tiles::of_expert(p, b - a);
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (e < p.E) l.cum[e] = x - n;
+    if (lane == 31) l.chunk[k] = x;
+  }
+  if (__syncthreads_or(bad)) return -1;
+  int x = lane < chunks ? l.chunk[lane] : 0;  // (at most 32 chunks)
+  const int own = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  const int n_tiles = __shfl_sync(0xffffffffu, x, 31);
+  for (int k = warp; k < chunks; k += kWarps) {
+    const int before = __shfl_sync(0xffffffffu, x - own, k);
+    if (32 * k + lane < p.E) l.cum[32 * k + lane] += before;
+  }
+  if (tid == 0) l.cum[p.E] = n_tiles;
+  const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = n_tiles - dealt;
+  for (int i = tid; i < cols; i += kGuThreads) l.hand[i] = 0;
+  __syncthreads();
+  if (whole > 0) {  // what each pair's whole tiles cost: a warp per expert, or all warps on each of a few
+    const bool few = p.E < kWarps;
+    for (int e = few ? 0 : warp; e < p.E; e += few ? 1 : kWarps) {
+      const int g0 = l.cum[e], g1 = min(l.cum[e + 1], dealt);
+      const int n_all = OP == G_DW ? p.n_out : l.off[e + 1] - l.off[e];
+      const int nt = Tiles::count(n_all), tn = nt ? Tiles::width(n_all, nt) : 0;
+      const long long steps = Tiles::steps(p, l.off[e + 1] - l.off[e]);
+      for (int g = g0 + (few ? tid : lane); g < g1; g += few ? kGuThreads : 32) {
+        const int t_n = (g - g0) % nt;
+        const long long c = steps * Tiles::cost(Tiles::padded(max(0, min(tn, n_all - t_n * tn))));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[g % cols]), (unsigned long long)c);
+      }
+    }
+  }
+  // the costs of the tiles that are split (at most kGuTailMost - 1 of them)
+  if (tid < tails) {
+    GuItem it;
+    Tiles::get(p, l, dealt + tid, it);
+    l.tail[tid] = (long long)it.nkb * it.cost;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long sum = 0;
+    for (int i0 = 0; i0 < tails; i0 += 32) {
+      const long long v = i0 + lane < tails ? l.tail[i0 + lane] : 0;
+      long long y = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      if (i0 + lane < tails) l.tail[i0 + lane] = sum + y - v;
+      sum += __shfl_sync(0xffffffffu, y, 31);
+    }
+    if (whole == 0) {
+      // pieces of one length, a tile cut into split_most on average at most
+      const long long pieces = max(1LL, min((long long)cols, (long long)tails * split_most));
+      for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * sum / pieces : sum;
+    } else {
+      // a piece brings its pair up to the mean of all pairs
+      long long hands = 0;
+      for (int i = lane; i < cols; i += 32) hands += l.hand[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) hands += __shfl_xor_sync(0xffffffffu, hands, o);
+      const long long mean = (sum + hands + cols - 1) / cols;
+      long long before = 0;
+      for (int i0 = 0; i0 < cols; i0 += 32) {
+        const long long v = i0 + lane < cols ? max(0LL, mean - l.hand[i0 + lane]) : 0;
+        long long y = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long z = __shfl_up_sync(0xffffffffu, y, o);
+          if (lane >= o) y += z;
+        }
+        if (i0 + lane < cols) l.cut[i0 + lane] = before + y - v;
+        before += __shfl_sync(0xffffffffu, y, 31);
+      }
+      const double scale = (double)sum / (double)max(1LL, before);
+      __syncwarp();
+      for (int i = lane; i < cols; i += 32) l.cut[i] = min(sum, (long long)((double)l.cut[i] * scale));
+      if (lane == 0) l.cut[cols] = sum;
+    }
+    if (lane == 0) l.tail[tails] = sum;
+  }
+  *whole_out = whole;
+  return n_tiles;
+}
 
 template <typename T>
 MOE_DEV T gu_cast(float v);
@@ -244,25 +439,24 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   const uint32_t raw32 = tc_smem(smem_raw);
   const uint32_t base = (raw32 + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - raw32);
-  constexpr uint32_t kScaleOff = kGuStages * 2 * kGuTile, kCumOff = kScaleOff + kGuScaleSlots * kGuN * 4,
-                     kLineOff = kCumOff + (kGmmMaxExperts + 1) * 8, kBarOff = kLineOff + sizeof(GuLine);
-  const uint32_t sc0 = base + kScaleOff, bar = base + kBarOff;
-  long long* cum = reinterpret_cast<long long*>(gen + kCumOff);
-  GuLine& line = *reinterpret_cast<GuLine*>(gen + kLineOff);
+  const uint32_t sc0 = base + kGuScaleOff, bar = base + kGuBarOff;
+  GuLine& line = *reinterpret_cast<GuLine*>(gen + kGuLineOff);
   // (L): used in the leader CTA only
-  auto full = [&](int s) { return bar + 8u * s; };                                   // (L) TMA bytes of both CTAs
-  auto empty = [&](int s) { return bar + 8u * (kGuStages + s); };                    // MMA commit
-  auto acc_full = [&](int b) { return bar + 8u * (2 * kGuStages + b); };             // MMA commit
-  auto acc_empty = [&](int b) { return bar + 8u * (2 * kGuStages + 2 + b); };        // (L) epilogue warps of both CTAs
-  auto sc_full = [&](int s) { return bar + 8u * (2 * kGuStages + 4 + s); };          // scale warp
-  auto sc_empty = [&](int s) { return bar + 8u * (2 * kGuStages + 4 + kGuScaleSlots + s); };  // epilogue warps
-  constexpr int kBars = 2 * kGuStages + 4 + 2 * kGuScaleSlots;
-  const uint32_t drain = bar + 8u * kBars;                                           // (L)
-  const uint32_t join = drain + 8u;                                                  // epilogue warps
-  int* tail = reinterpret_cast<int*>(gen + (bar - base) + 8 * (kBars + 2));
+  auto full = [&](int s) { return bar + 8u * s; };                                      // (L) TMA bytes of both CTAs
+  auto empty = [&](int s) { return bar + 8u * (kGuStages + s); };                       // MMA commit
+  auto acc_full = [&](int b) { return bar + 8u * (2 * kGuStages + b); };                // MMA commit
+  auto acc_empty = [&](int b) { return bar + 8u * (2 * kGuStages + kGuSegs + b); };     // (L) epilogue warps, both CTAs
+  constexpr int kBarSc = 2 * kGuStages + 2 * kGuSegs;
+  auto sc_full = [&](int s) { return bar + 8u * (kBarSc + s); };                        // scale warp
+  auto sc_empty = [&](int s) { return bar + 8u * (kBarSc + kGuScaleSlots + s); };       // epilogue warps
+  constexpr int kBars = kBarSc + 2 * kGuScaleSlots;
+  const uint32_t drain = bar + 8u * kBars;                                              // (L)
+  const uint32_t join = drain + 8u;                                                     // epilogue warps
+  int* tail = reinterpret_cast<int*>(gen + kGuBarOff + 8 * (kBars + 2));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = tail + 1;
   int* last_flag = tail + 2;
+  static_assert(8 * (kBars + 2) + 12 <= 512, "barrier block");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, pair, npairs;
@@ -277,7 +471,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       tc_bar_init(full(s), 1);
       tc_bar_init(empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kGuSegs; ++b) {
       tc_bar_init(acc_full(b), 1);
       tc_bar_init(acc_empty(b), 2 * kGuEpiWarps);
     }
@@ -296,262 +490,215 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  using Tiles = GuTiles<OP, KE>;
   using Walk = GuWalk<OP, KE>;
   const int m_all = OP == G_MM ? g.n_out : g.n_in;
   const int cols = (int)npairs;
-  const bool plan_ok = gmm_plan(
-      g, [&](int rows) -> long long { return Tiles::of_expert(g, rows); }, cum, &line.flag);
-  const int n_tiles = plan_ok ? (int)cum[g.E] : 0;
-  for (int i = tid; i <= cols; i += kGuThreads) line.col[i] = 0;
-  if (tid == 0) {
-    line.cost_most = 0;
-    line.start_pos = 0;
-    line.start_col = line.start_row = 0;
-  }
-  __syncthreads();
-  for (int t = tid; t < n_tiles; t += kGuThreads) {  // the cost of each hand
-    GuItem it;
-    Tiles::get(g, cum, t, it);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&line.col[t % cols]), (unsigned long long)it.nkb * it.cost);
-    atomicMax(reinterpret_cast<unsigned long long*>(&line.cost_most), (unsigned long long)it.cost);
-  }
-  __syncthreads();
-  if (warp == 0) {  // hands one after the other
-    long long sum = 0;
-    for (int c0 = 0; c0 < cols; c0 += 32) {
-      const long long v = c0 + lane < cols ? line.col[c0 + lane] : 0;
-      long long x = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (c0 + lane < cols) line.col[c0 + lane] = sum + x - v;
-      sum += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) line.col[cols] = sum;
-  }
-  __syncthreads();
-  // Pieces: one per pair, none shorter than a step (each piece that a tile
-  // reaches into then holds a step of it), a tile cut into split_most at most.
-  const long long total = line.col[cols];
-  long long pieces = 0;
-  if (total > 0) {
-    pieces = min((long long)cols, total / line.cost_most);
-    pieces = min(pieces, (long long)n_tiles * p.split_most);
-  }
-  const long long begin = pair < pieces ? (long long)pair * total / pieces : 0;
-  const long long end = pair < pieces ? ((long long)pair + 1) * total / pieces : 0;
-  auto piece_of = [&](long long u) { return (int)(((u + 1) * pieces - 1) / total); };
-  if (warp == 0 && begin < end) {  // the piece's first tile
-    int c = 0;
-    for (int c0 = 0; c0 < cols; c0 += 32)
-      c += __popc(__ballot_sync(0xffffffffu, c0 + lane < cols && line.col[c0 + lane + 1] <= begin));
-    long long at = line.col[c];
-    for (int row = 0;; row += 32) {
-      const long long t = (long long)(row + lane) * cols + c;
-      long long w = 0;
-      if (t < n_tiles) {
-        GuItem it;
-        Tiles::get(g, cum, (int)t, it);
-        w = (long long)it.nkb * it.cost;
-      }
-      long long x = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t here = __ballot_sync(0xffffffffu, w > 0 && at + x > begin);
-      if (here) {
-        if (lane == __ffs(here) - 1) {
-          line.start_pos = at + x - w;
-          line.start_col = c;
-          line.start_row = row + lane;
-        }
-        break;
-      }
-      at += __shfl_sync(0xffffffffu, x, 31);
-      if ((long long)(row + 32) * cols + c >= n_tiles) break;  // not reached: begin lies in this hand
-    }
-  }
+  int whole = 0;
+  const int planned = gu_plan<OP, KE>(g, line, cols, p.split_most, &whole);
+  if (planned < 0 && tid == 0) set_error(g.err, kErrDeviceInput);
+  const int n_tiles = max(planned, 0);
   tc_fence_before();
   __syncthreads();
+  if (planned < 0 && tid < 2) line.cut[pair + tid] = 0;
   cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated before any cross-CTA use
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    // ================= TMA issuer of this CTA's halves of both operands
-    if (lane == 0) {
-      um_prefetch_map(&p.a_map);
-      Walk walk(g, cum, line, cols, begin, end);
-      GuItem it;
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      while (ok && walk.next(it)) {
-        if (it.none) continue;
-        const int half = it.np >> 1;
-        const int m = it.m0 + (int)rank * 128;
-        const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-        const int panels = (half + 63) >> 6;  // dw
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          if (!cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t a = base + (uint32_t)st * 2 * kGuTile, b = a + kGuTile;
-          const uint32_t fb = cl_addr(full(st), 0);
-          if constexpr (OP != G_DW) {
-            if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (16 << bx) * 128)));
-            if constexpr (OP == G_MM) {
-              gu_tma_3d(a, &p.a_map, kb * KE, m, it.e, fb);
-            } else {
-              gu_tma_3d(a, &p.a_map, m, kb * KE, it.e, fb);
-              gu_tma_3d(a + 8192, &p.a_map, m + 64, kb * KE, it.e, fb);
-            }
-            gu_tma_2d(b, &p.b_map[bx], kb * KE, it.n0 + (int)rank * half, fb);
-          } else {
-            const int y = it.r0 + kb * KE, left = it.r1 - y, n = it.n0 + (int)rank * half;
-            if (left >= KE) {
-              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + panels * 8192)));
-              gu_tma_2d(a, &p.a_map, m, y, fb);
-              gu_tma_2d(a + 8192, &p.a_map, m + 64, y, fb);
-              for (int q = 0; q < panels; ++q) gu_tma_2d(b + q * 8192, &p.b_map[0], n + 64 * q, y, fb);
-            } else {
-              const int fill = (left + 15) & ~15;
-              if (leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (2 + panels)));
-              for (int q = 0; q < 2 + panels; ++q) {
-                const bool isa = q < 2;
-                const uint32_t dst = isa ? a + q * 8192 : b + (q - 2) * 8192;
-                const int x = isa ? m + 64 * q : n + 64 * (q - 2);
-                const CUtensorMap* maps = isa ? p.a_tail : p.b_tail;
-                int r = 0;
-                for (; r + 8 <= left; r += 8) gu_tma_2d(dst + r * 128, &maps[0], x, y + r, fb);
-                for (; r & 7 || r < left; ++r)  // rows beyond the expert's: from beyond the tensor, zeros
-                  gu_tma_2d(dst + r * 128, &maps[1], x, r < left ? y + r : g.rows, fb);
-                if (r < fill) gu_tma_2d(dst + r * 128, &maps[0], x, g.rows, fb);
-              }
-            }
-          }
-          if (++st == kGuStages) st = 0, ph ^= 1u;
-        }
-      }
-      if (!ok) {  // a wait gave up: let the copies in flight land before this CTA's memory is released
-        const long long t0 = clock64();
-        while (clock64() - t0 < kGuLinger) {
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ================= MMA issuer (leader CTA)
-    if (leader && lane == 0) {
-      Walk walk(g, cum, line, cols, begin, end);
-      GuItem it;
-      int st = 0, seg = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      const uint32_t idesc0 = (1u << 4) | ((uint32_t)(p.type == G_BF16 ? 1 : 0) * ((1u << 7) | (1u << 10))) |
-                              ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (16u << 24);
-      const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + kGuTile, B_MN);
-      while (ok && walk.next(it)) {
-        if (it.none) continue;
-        const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
-        for (int kb = it.kb0; kb < it.kb1;) {
-          const int kend = CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
-          const int buf = seg & 1;
-          if (!cl_bar_wait(acc_empty(buf), ((seg >> 1) & 1) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)buf * kGuN;
-          uint32_t acc = 0;
-          for (; kb < kend; ++kb) {
-            if (!cl_bar_wait(full(st), ph, abort_flag)) {
+  if (warp < 4) {
+    // the sums of CHAIN > 0 are the epilogue's registers (the host checks that the block has kGuRegs per thread)
+    if constexpr (CHAIN > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
+    if (warp == 0) {
+      // ================= TMA issuer of this CTA's halves of both operands
+      if (lane == 0) {
+        um_prefetch_map(&p.a_map);
+        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+        GuItem it;
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        while (ok && walk.next(it)) {
+          if (it.none) continue;
+          const int half = it.np >> 1;
+          const int m = it.m0 + (int)rank * 128;
+          const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+          const int panels = (half + 63) >> 6;  // dw
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            if (!cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint64_t so = (uint64_t)((uint32_t)st * 2 * kGuTile >> 4);
-            int steps = 4;
-            if constexpr (OP == G_DW) steps = min(4, (it.r1 - it.r0 - kb * KE + 15) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (OP != G_DW || k < steps) {
-                // 16 (e4m3: 32) contracted values: 32 bytes along a K-major row, 16 rows of a panel otherwise
-                gu_mma<FP8>(d, da0 + so + (uint64_t)((A_MN ? 2048 : 32) * k >> 4),
-                            db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
-                acc = 1;
+            const uint32_t a = base + (uint32_t)st * 2 * kGuTile, b = a + kGuTile;
+            const uint32_t fb = cl_addr(full(st), 0);
+            if constexpr (OP != G_DW) {
+              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (16 << bx) * 128)));
+              if constexpr (OP == G_MM) {
+                gu_tma_3d(a, &p.a_map, kb * KE, m, it.e, fb);
+              } else {
+                gu_tma_3d(a, &p.a_map, m, kb * KE, it.e, fb);
+                gu_tma_3d(a + 8192, &p.a_map, m + 64, kb * KE, it.e, fb);
               }
-            umma2_commit_both(empty(st));
+              gu_tma_2d(b, &p.b_map[bx], kb * KE, it.n0 + (int)rank * half, fb);
+            } else {
+              const int y = it.r0 + kb * KE, left = it.r1 - y, n = it.n0 + (int)rank * half;
+              if (left >= KE) {
+                if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + panels * 8192)));
+                gu_tma_2d(a, &p.a_map, m, y, fb);
+                gu_tma_2d(a + 8192, &p.a_map, m + 64, y, fb);
+                for (int q = 0; q < panels; ++q) gu_tma_2d(b + q * 8192, &p.b_map[0], n + 64 * q, y, fb);
+              } else {
+                const int fill = (left + 15) & ~15;
+                if (leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (2 + panels)));
+                for (int q = 0; q < 2 + panels; ++q) {
+                  const bool isa = q < 2;
+                  const uint32_t dst = isa ? a + q * 8192 : b + (q - 2) * 8192;
+                  const int x = isa ? m + 64 * q : n + 64 * (q - 2);
+                  const CUtensorMap* maps = isa ? p.a_tail : p.b_tail;
+                  int r = 0;
+                  for (; r + 8 <= left; r += 8) gu_tma_2d(dst + r * 128, &maps[0], x, y + r, fb);
+                  for (; r & 7 || r < left; ++r)  // rows beyond the expert's: from beyond the tensor, zeros
+                    gu_tma_2d(dst + r * 128, &maps[1], x, r < left ? y + r : g.rows, fb);
+                  if (r < fill) gu_tma_2d(dst + r * 128, &maps[0], x, g.rows, fb);
+                }
+              }
+            }
             if (++st == kGuStages) st = 0, ph ^= 1u;
           }
-          if (!ok) break;
-          umma2_commit_both(acc_full(buf));
-          ++seg;
         }
-      }
-      umma2_commit_both(drain);
-      const long long t0 = clock64();
-      while (!cl_bar_try(drain, 0) && clock64() - t0 < kTcWaitCycles) {
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ================= 8-bit product: the scales of each step, row scale times this CTA's weight scale
-    if constexpr (FP8) {
-      Walk walk(g, cum, line, cols, begin, end);
-      GuItem it;
-      int slot = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      const int groups = (g.n_in + 127) >> 7;
-      constexpr int AHEAD = 4;  // steps whose loads are in flight together
-      while (ok && walk.next(it)) {
-        const int ob = (it.m0 >> 7) + (int)rank;
-        const float* swp = g.sw + ((long long)it.e * ((g.n_out + 127) >> 7) + ob) * groups;
-        const bool live = ob * 128 < g.n_out;
-        const float* sxp = g.sx + it.n0;
-        for (int k0 = it.kb0; k0 < it.kb1 && ok; k0 += AHEAD) {
-          float v[AHEAD][8], w[AHEAD];
-#pragma unroll
-          for (int a = 0; a < AHEAD; ++a) {
-            const int kb = min(k0 + a, it.kb1 - 1);
-            w[a] = live ? __ldg(swp + kb) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int c = lane + 32 * j;
-              v[a][j] = c < it.nv ? __ldg(sxp + (long long)kb * g.rows + c) : 0.f;
-            }
-          }
-#pragma unroll
-          for (int a = 0; a < AHEAD; ++a) {
-            if (k0 + a >= it.kb1) break;
-            ok = cl_bar_wait(sc_empty(slot), ph ^ 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
-            const uint32_t dst = sc0 + (uint32_t)slot * kGuN * 4 + 4u * lane;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 128u * j), "f"(v[a][j] * w[a]) : "memory");
-            __syncwarp();
-            if (lane == 0) tc_bar_arrive(sc_full(slot));
-            if (++slot == kGuScaleSlots) slot = 0, ph ^= 1u;
+        if (!ok) {  // a wait gave up: let the copies in flight land before this CTA's memory is released
+          const long long t0 = clock64();
+          while (clock64() - t0 < kGuLinger) {
           }
         }
       }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ================= MMA issuer (leader CTA)
+      if (leader && lane == 0) {
+        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+        GuItem it;
+        int st = 0, seg = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        GuRing ring;
+        int user[kGuSegs];  // the last sum in each TMEM slot
+        int done = -1;      // the latest sum known to be through the epilogue
+  #pragma unroll
+        for (int i = 0; i < kGuSegs; ++i) user[i] = -1;
+        const uint32_t idesc0 = (1u << 4) | ((uint32_t)(p.type == G_BF16 ? 1 : 0) * ((1u << 7) | (1u << 10))) |
+                                ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (16u << 24);
+        const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + kGuTile, B_MN);
+        while (ok && walk.next(it)) {
+          if (it.none) continue;
+          const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
+          for (int kb = it.kb0; kb < it.kb1;) {
+            const int kend = CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
+            // The sums leave the epilogue in order, so all that used these
+            // slots or this barrier (eight sums ago) are through once the
+            // latest of them is.  One already seen through is not waited for
+            // again: its barrier may be phases ahead.
+            const int at = ring.take(it.np);
+            int before = seg - kGuSegs;
+#pragma unroll
+            for (int i = 0; i < kGuSegs; ++i)
+              if (i >= at && i < at + ring.used) {
+                before = max(before, user[i]);
+                user[i] = seg;
+              }
+            if (before > done) {
+              if (!cl_bar_wait(acc_empty(before & (kGuSegs - 1)), (uint32_t)(before / kGuSegs) & 1u, abort_flag)) {
+                ok = false;
+                break;
+              }
+              done = before;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)at * kGuSlotCols;
+            uint32_t acc = 0;
+            for (; kb < kend; ++kb) {
+              if (!cl_bar_wait(full(st), ph, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t so = (uint64_t)((uint32_t)st * 2 * kGuTile >> 4);
+              int steps = 4;
+              if constexpr (OP == G_DW) steps = min(4, (it.r1 - it.r0 - kb * KE + 15) >> 4);
+  #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (OP != G_DW || k < steps) {
+                  // 16 (e4m3: 32) contracted values: 32 bytes along a K-major row, 16 rows of a panel otherwise
+                  gu_mma<FP8>(d, da0 + so + (uint64_t)((A_MN ? 2048 : 32) * k >> 4),
+                              db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
+                  acc = 1;
+                }
+              umma2_commit_both(empty(st));
+              if (++st == kGuStages) st = 0, ph ^= 1u;
+            }
+            if (!ok) break;
+            umma2_commit_both(acc_full(seg & (kGuSegs - 1)));
+            ++seg;
+          }
+        }
+        umma2_commit_both(drain);
+        const long long t0 = clock64();
+        while (!cl_bar_try(drain, 0) && clock64() - t0 < kTcWaitCycles) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ================= 8-bit product: the scales of each step, row scale times this CTA's weight scale
+      if constexpr (FP8) {
+        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+        GuItem it;
+        int slot = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const int groups = (g.n_in + 127) >> 7;
+        constexpr int AHEAD = 4;  // steps whose loads are in flight together
+        while (ok && walk.next(it)) {
+          const int ob = (it.m0 >> 7) + (int)rank;
+          const float* swp = g.sw + ((long long)it.e * ((g.n_out + 127) >> 7) + ob) * groups;
+          const bool live = ob * 128 < g.n_out;
+          const float* sxp = g.sx + it.n0;
+          for (int k0 = it.kb0; k0 < it.kb1 && ok; k0 += AHEAD) {
+            float v[AHEAD][8], w[AHEAD];
+  #pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+              const int kb = min(k0 + a, it.kb1 - 1);
+              w[a] = live ? __ldg(swp + kb) : 0.f;
+  #pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int c = lane + 32 * j;
+                v[a][j] = c < it.nv ? __ldg(sxp + (long long)kb * g.rows + c) : 0.f;
+              }
+            }
+  #pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+              if (k0 + a >= it.kb1) break;
+              ok = cl_bar_wait(sc_empty(slot), ph ^ 1u, abort_flag);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              const uint32_t dst = sc0 + (uint32_t)slot * kGuN * 4 + 4u * lane;
+  #pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 128u * j), "f"(v[a][j] * w[a]) : "memory");
+              __syncwarp();
+              if (lane == 0) tc_bar_arrive(sc_full(slot));
+              if (++slot == kGuScaleSlots) slot = 0, ph ^= 1u;
+            }
+          }
+        }
+      }
     }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (CHAIN > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every other 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
-    Walk walk(g, cum, line, cols, begin, end);
+    Walk walk(g, line, (int)pair, cols, n_tiles, whole);
     GuItem it;
+    GuRing ring;
     int seg = 0, slot = 0;
     uint32_t sph = 0, jph = 0;
     auto epi_sync = [&]() {  // the epilogue warps meet (bounded, unlike a hardware barrier)
@@ -563,9 +710,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     };
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
     unsigned* counters = reinterpret_cast<unsigned*>(p.ws + kGuCounters);
+    // a partial tile: four columns (16 bytes) of each M value together
     auto part_of = [&](int piece, int which) {
-      return reinterpret_cast<float*>(p.ws + kGuParts + (size_t)((piece * 2 + (int)rank) * 2 + which) * kGuPart) + 32 * q +
-             lane;
+      return reinterpret_cast<float4*>(p.ws + kGuParts + (size_t)((piece * 2 + (int)rank) * 2 + which) * kGuPart) +
+             32 * q + lane;
     };
     bool ok = true;
     while (ok && walk.next(it)) {
@@ -573,14 +721,15 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       const int m = it.m0 + (int)rank * 128 + 32 * q + lane;
       const long long ld = OP == G_DW ? g.n_in : g.ld_out;
       const long long ob = (OP == G_DW ? ((long long)it.e * g.n_out + it.n0) * g.n_in : (long long)it.n0 * g.ld_out) + m;
-      const bool whole = it.kb0 == 0 && it.kb1 == it.nkb;
-      float* part = part_of((int)pair, it.kb0 > 0 ? 0 : 1);
+      const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
       auto put = [&](int c, const float (&v)[32]) {
-        if (whole) {
+        if (all) {
           if (m < m_all) gu_store32(g.out, g.out_type, ob + 32 * c * ld, ld, it.nv - 32 * c, v);
         } else {
+          float4* part = part_of((int)pair, it.kb0 > 0 ? 0 : 1) + 8 * c * 128;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) __stcg(part + (32 * c + i) * 128, v[i]);
+          for (int i = 0; i < 8; ++i)
+            __stcg(part + i * 128, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
       };
       if (it.none) {
@@ -592,28 +741,29 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         continue;
       }
       if constexpr (CHAIN == 0) {
-        const int buf = seg & 1;
-        ok = cl_bar_wait(acc_full(buf), (seg >> 1) & 1, abort_flag);
+        const int b = seg & (kGuSegs - 1), at = ring.take(it.np);
+        ok = cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         for (int c = h; c < chunks; c += 2) {
           float v[32];
-          gu_ld32(lane_addr + (uint32_t)(buf * kGuN + 32 * c), v);
+          gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
           put(c, v);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cl_arrive(cl_addr(acc_empty(buf), 0));
+        if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
         ++seg;
       } else {
-        float acc[4][32];
+        // sums in pairs of columns, for the packed fp32 instructions
+        unsigned long long acc[4][16];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
+          for (int i = 0; i < 16; ++i) acc[j][i] = 0;
         for (int kb = it.kb0; kb < it.kb1; kb += CHAIN) {
-          const int buf = seg & 1;
-          ok = cl_bar_wait(acc_full(buf), (seg >> 1) & 1, abort_flag);
+          const int b = seg & (kGuSegs - 1), at = ring.take(it.np);
+          ok = cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
           if (FP8) ok = ok && tc_bar_wait(sc_full(slot), sph, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -621,23 +771,22 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           }
           tc_fence_after();
           const uint32_t sp = sc0 + (uint32_t)slot * kGuN * 4;
+          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c = 2 * j + h;
             if (c < chunks) {
               float v[32];
-              gu_ld32(lane_addr + (uint32_t)(buf * kGuN + 32 * c), v);
+              gu_ld32(ta + 32u * c, v);
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 if constexpr (FP8) {
-                  const uint4 s = tc_lds128(sp + (uint32_t)(32 * c + i) * 4);
-                  acc[j][i] = fmaf(v[i], __uint_as_float(s.x), acc[j][i]);
-                  acc[j][i + 1] = fmaf(v[i + 1], __uint_as_float(s.y), acc[j][i + 1]);
-                  acc[j][i + 2] = fmaf(v[i + 2], __uint_as_float(s.z), acc[j][i + 2]);
-                  acc[j][i + 3] = fmaf(v[i + 3], __uint_as_float(s.w), acc[j][i + 3]);
+                  const ulonglong2 s = gu_lds_u64x2(sp + (uint32_t)(32 * c + i) * 4);
+                  gu_fma2(acc[j][i / 2], gu_pack(v[i], v[i + 1]), s.x);
+                  gu_fma2(acc[j][i / 2 + 1], gu_pack(v[i + 2], v[i + 3]), s.y);
                 } else {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) acc[j][i + k] += v[i + k];
+                  gu_add2(acc[j][i / 2], gu_pack(v[i], v[i + 1]));
+                  gu_add2(acc[j][i / 2 + 1], gu_pack(v[i + 2], v[i + 3]));
                 }
               }
             }
@@ -645,7 +794,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            cl_arrive(cl_addr(acc_empty(buf), 0));
+            cl_arrive(cl_addr(acc_empty(b), 0));
             if (FP8) tc_bar_arrive(sc_empty(slot));
           }
           ++seg;
@@ -654,19 +803,45 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (2 * j + h < chunks) put(2 * j + h, acc[j]);
+          if (2 * j + h < chunks) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) gu_unpack(acc[j][i], v[2 * i], v[2 * i + 1]);
+            put(2 * j + h, v);
+          }
       }
-      if (!whole) {
-        // count this part in; the last part's CTA adds them all, in the pieces' order
-        const int first = piece_of(it.pos), last = piece_of(it.pos + (long long)(it.nkb - 1) * it.cost);
+      if (!all) {
+        // Count this part in; the last part's CTA adds them all, in the
+        // pieces' order.  The parts are those of the pieces from the one that
+        // holds the tile's first step to the one that holds its last, less
+        // those too short to hold a step.
+        auto piece_at = [&](long long u) {
+          int lo = 0, hi = cols;  // cut[lo] <= u < cut[hi]
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (line.cut[mid] <= u) lo = mid;
+            else hi = mid;
+          }
+          return lo;
+        };
+        const int first = piece_at(it.pos), last = piece_at(it.pos + (long long)(it.nkb - 1) * it.cost);
+        uint32_t has[3] = {0, 0, 0};
+        int parts = 0;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int s = first + 32 * k + lane;
+          const bool in = s <= last && Walk::steps_before(line.cut[s], it) < Walk::steps_before(line.cut[s + 1], it);
+          has[k] = __ballot_sync(0xffffffffu, in);
+          parts += __popc(has[k]);
+        }
         __threadfence();
         ok = epi_sync();
         if (!ok) break;
         if (tid == 128) {
           unsigned* ctr = counters + first * 2 + rank;
           const unsigned before = atomicAdd(ctr, 1u);
-          *last_flag = before == (unsigned)(last - first);
-          if (before == (unsigned)(last - first)) *ctr = 0;
+          *last_flag = before + 1 == (unsigned)parts;
+          if (before + 1 == (unsigned)parts) *ctr = 0;
         }
         ok = epi_sync();
         if (!ok) break;
@@ -678,12 +853,37 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           for (int c = h; c < chunks; c += 2) {
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __ldcg(part_of(first, 1) + (32 * c + i) * 128);
-            for (int s = first + 1; s <= last; ++s) {
-              const float* src = part_of(s, 0);
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += __ldcg(src + (32 * c + i) * 128);
-            }
+            for (int k = 0; k < 3; ++k)
+              for (uint32_t left = has[k]; left;) {
+                // two parts' loads in flight together
+                const int s0 = first + 32 * k + __ffs(left) - 1;
+                left &= left - 1;
+                const int s1 = left ? first + 32 * k + __ffs(left) - 1 : -1;
+                left &= left - 1;
+                const float4* p0 = part_of(s0, s0 == first ? 1 : 0) + 8 * c * 128;
+                const float4* p1 = part_of(s1 < 0 ? s0 : s1, s1 < 0 && s0 == first ? 1 : 0) + 8 * c * 128;
+                float4 a[8], b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  a[i] = __ldcg(p0 + i * 128);
+                  b[i] = __ldcg(p1 + i * 128);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  v[4 * i] += a[i].x;
+                  v[4 * i + 1] += a[i].y;
+                  v[4 * i + 2] += a[i].z;
+                  v[4 * i + 3] += a[i].w;
+                  if (s1 >= 0) {
+                    v[4 * i] += b[i].x;
+                    v[4 * i + 1] += b[i].y;
+                    v[4 * i + 2] += b[i].z;
+                    v[4 * i + 3] += b[i].w;
+                  }
+                }
+              }
             if (m < m_all) gu_store32(g.out, g.out_type, ob + 32 * c * ld, ld, it.nv - 32 * c, v);
           }
         }

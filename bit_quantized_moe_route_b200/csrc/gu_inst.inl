@@ -35,6 +35,13 @@ int gu_pairs<GU_OP, GU_FP8, GU_CHAIN>() {
     cudaGetLastError();
     return 0;
   }
+  // the register hand-over of these kernels counts on what the block starts with
+  cudaFuncAttributes fa;
+  if (GU_CHAIN > 0 && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_CHAIN>) != cudaSuccess ||
+                       fa.numRegs != kGuRegs)) {
+    cudaGetLastError();
+    return 0;
+  }
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
   int n = 0;

@@ -169,6 +169,19 @@ def test_many_experts(cuda_device, ws, op):
     run_op(op, counts, 64, 72, BF, BF, cuda_device, ws)
 
 
+@pytest.mark.parametrize("op", ["mm", "dx", "fp8"])
+@pytest.mark.parametrize("seed", range(3))
+def test_mixed_tile_widths(cuda_device, ws, op, seed):
+    """Row counts that make tiles of every width follow one another many times over in one launch: narrow and wide
+    accumulators share tensor memory in changing patterns."""
+    g = np.random.default_rng(seed)
+    counts = [int(g.choice([1, 20, 33, 64, 65, 128, 129, 200, 256, 300])) for _ in range(60)]
+    if op == "fp8":
+        run_fp8(counts, 256, 2048, BF, cuda_device, ws)
+    else:
+        run_op(op, counts, *((128, 2048) if op == "mm" else (2048, 128)), BF, BF if seed else FP, cuda_device, ws)
+
+
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("aligned", [True, False])
 def test_same_bits_every_time(cuda_device, ws, op, aligned):
