@@ -41,7 +41,15 @@
 //
 // CHAIN = 0: the tile's whole sum is taken in tensor memory.  CHAIN > 0: every
 // CHAIN steps the sum is handed to the epilogue warps, which add it to sums in
-// registers with ordinary fp32 additions, scaled for the 8-bit product.
+// registers with ordinary fp32 additions.
+//
+// The 8-bit product hands over every step (CHAIN = 1), since its scales change
+// there: register sum += scale[row] * step sum, on pairs of columns (packed
+// fp32 instructions).  The hand-over costs some 2,000 cycles there and back
+// (commit, barriers of two CTAs, TMEM reads) against 512 for the MMA of a
+// 256-row tile, so a half of tensor memory holds one step of a wide tile, two
+// of a tile of up to 128 rows or four of up to 64, handed over together, and
+// is given back when its last values are in registers.
 #pragma once
 
 #include <cuda.h>
@@ -54,12 +62,14 @@ namespace moe {
 constexpr int kGuStages = 6;
 constexpr int kGuTile = 16384;            // bytes of one operand of one step
 constexpr int kGuN = 256;                 // output rows per tile
-constexpr int kGuThreads = 384;           // warps: 0 loads, 1 MMA, 2 scales, 4-11 epilogue
+constexpr int kGuThreads = 384;           // warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 epilogue
 constexpr int kGuEpiWarps = 8;
 constexpr int kGuRegs = 168;              // registers per thread at launch
 constexpr int kGuRegsLow = 88, kGuRegsHigh = 208;  // CHAIN > 0: warps 0-3, epilogue warps
 static_assert(128 * kGuRegsLow + 256 * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
-constexpr int kGuScaleSlots = 8;
+constexpr int kGuScaleSlots = 4;
+constexpr int kGuItems = 4;               // items handed out ahead
+constexpr int kGuStageRows = 16;          // output rows that a warp stores together
 constexpr int kGuSegs = 8;                // sums between the MMA and the epilogue; TMEM slots
 constexpr int kGuSlotCols = 512 / kGuSegs;
 constexpr int kGuPart = 128 * kGuN * 4;   // bytes of one partial tile of one CTA
@@ -68,6 +78,7 @@ constexpr long long kGuLinger = 4000000;  // ~2 ms
 constexpr size_t kGuCounters = 1024;      // workspace: counters, then the partial tiles
 constexpr size_t kGuParts = 4096;
 constexpr size_t kGuWsBytes = size_t(40) << 20;
+static_assert(kGuPairsMax <= 96, "the plan's threads");
 static_assert(kGuCounters + kGuPairsMax * 2 * 4 <= kGuParts, "counters");
 static_assert(kGuParts + (size_t)kGuPairsMax * 4 * kGuPart <= kGuWsBytes, "workspace");
 
@@ -131,6 +142,34 @@ MOE_DEV void gu_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// the same, without the wait: v is complete after gu_ld_wait
+MOE_DEV void gu_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+MOE_DEV void gu_ld_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// waits for every load issued; r's uses stay behind it
+template <int W>
+MOE_DEV void gu_ld_wait(uint32_t (&r)[W]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < W; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // two fp32 in one register pair, and the packed instructions on them
 MOE_DEV unsigned long long gu_pack(float lo, float hi) {
   unsigned long long r;
@@ -143,40 +182,58 @@ MOE_DEV void gu_unpack(unsigned long long v, float& lo, float& hi) {
 MOE_DEV void gu_fma2(unsigned long long& c, unsigned long long a, unsigned long long b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
-MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
 MOE_DEV ulonglong2 gu_lds_u64x2(uint32_t a) {
   ulonglong2 v;
   asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
   return v;
 }
-
+// W step sums times their columns' scales into register sums c0, c0 + 1, ...
+template <int W>
+MOE_DEV void gu_scaled(unsigned long long (&acc)[16], const int c0, const uint32_t (&r)[W], uint32_t scales) {
+#pragma unroll
+  for (int i = 0; i < W; i += 4) {
+    const ulonglong2 s = gu_lds_u64x2(scales + 4u * i);
+    gu_fma2(acc[(c0 + i) / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s.x);
+    gu_fma2(acc[(c0 + i) / 2 + 1], gu_pack(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), s.y);
+  }
+}
+MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
 // ------------------------------------------------------------ work items
 // A run of steps of one tile.
-struct GuItem {
-  int e, m0, n0, nv, np;   // expert, first M value, first output row (dw: first o), rows in use, MMA width
-  int kb0, kb1, nkb;       // steps, and the tile's number of steps
-  int cost;                // of one step
-  int r0, r1;              // dw: the expert's rows
-  bool none;               // dw: no rows; one step that reads nothing, zeros to write
+struct alignas(16) GuItem {
+  int e, m0, n0, nv;       // expert, first M value, first output row (dw: first o), rows in use
+  int np, kb0, kb1, nkb;   // MMA width, steps, the tile's number of steps
+  int cost, r0, r1;        // of one step; dw: the expert's rows
+  int kind;                // GuKind
   long long pos;           // where the tile begins on the line
+  long long pad;
+};
+static_assert(sizeof(GuItem) == 64, "four 16-byte pieces");
+enum GuKind : int {
+  GU_RUN = 0,
+  GU_ZEROS = 1,  // dw: an expert without rows; one step that reads nothing, zeros to write
+  GU_STOP = 2    // no more items
 };
 
 constexpr int kGuTailMost = 2 * kGuPairsMax;
 
 // The plan of a launch (shared memory of each CTA; the same in all of them).
-struct GuLine {
+struct alignas(16) GuLine {
   long long tail[kGuTailMost + 1];  // the tiles that are split: where each begins on the line of costs
   long long cut[kGuPairsMax + 1];   // where each pair's piece of that line begins
   long long hand[kGuPairsMax];      // cost of the tiles that each pair has whole
+  GuItem item[kGuItems];
   int off[kGmmMaxExperts + 1];      // the experts' rows
   int cum[kGmmMaxExperts + 1];      // the experts' tiles
   int chunk[kGmmMaxExperts / 32];
 };
 
-// shared memory from the first 1024-byte boundary: operand ring, scales, plan, barriers
+// shared memory from the first 1024-byte boundary: operand ring, scales, the
+// epilogue's rows on their way out, plan, barriers
 constexpr uint32_t kGuScaleOff = kGuStages * 2 * kGuTile;
-constexpr uint32_t kGuLineOff = kGuScaleOff + kGuScaleSlots * kGuN * 4;
-constexpr uint32_t kGuBarOff = (kGuLineOff + sizeof(GuLine) + 7) / 8 * 8;
+constexpr uint32_t kGuOutOff = kGuScaleOff + kGuScaleSlots * kGuN * 4;
+constexpr uint32_t kGuLineOff = kGuOutOff + kGuEpiWarps * kGuStageRows * 128;
+constexpr uint32_t kGuBarOff = kGuLineOff + sizeof(GuLine);
 constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
@@ -220,7 +277,7 @@ struct GuTiles {
     it.np = padded(it.nv);
     it.n0 = OP == G_DW ? n_begin : it.r0 + n_begin;
     it.nkb = steps(p, it.r1 - it.r0);
-    it.none = OP == G_DW && it.r1 == it.r0;
+    it.kind = OP == G_DW && it.r1 == it.r0 ? GU_ZEROS : GU_RUN;
     it.cost = cost(it.np);
   }
 };
@@ -235,6 +292,10 @@ struct GuRing {
     return at;
   }
 };
+
+// 8-bit product: columns per step in a half of tensor memory; the half holds
+// 256 / stride steps.
+MOE_DEV int gu_stride(int np) { return np <= 64 ? 64 : np <= 128 ? 128 : 256; }
 
 // Walks a pair's work; every warp that does, and both CTAs of the pair, see the same items.
 template <int OP, int KE>
@@ -338,18 +399,19 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
   const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = n_tiles - dealt;
   for (int i = tid; i < cols; i += kGuThreads) l.hand[i] = 0;
   __syncthreads();
-  if (whole > 0) {  // what each pair's whole tiles cost: a warp per expert, or all warps on each of a few
-    const bool few = p.E < kWarps;
-    for (int e = few ? 0 : warp; e < p.E; e += few ? 1 : kWarps) {
-      const int g0 = l.cum[e], g1 = min(l.cum[e + 1], dealt);
-      const int n_all = OP == G_DW ? p.n_out : l.off[e + 1] - l.off[e];
-      const int nt = Tiles::count(n_all), tn = nt ? Tiles::width(n_all, nt) : 0;
-      const long long steps = Tiles::steps(p, l.off[e + 1] - l.off[e]);
-      for (int g = g0 + (few ? tid : lane); g < g1; g += few ? kGuThreads : 32) {
-        const int t_n = (g - g0) % nt;
-        const long long c = steps * Tiles::cost(Tiles::padded(max(0, min(tn, n_all - t_n * tn))));
-        atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[g % cols]), (unsigned long long)c);
+  // What each pair's whole tiles cost.  mm, dx: as good as the same for all
+  // pairs.  dw: a tile's steps are its expert's rows.
+  if (OP == G_DW && whole > 0) {
+    const int q = tid % 96, part = tid / 96;
+    if (q < cols) {
+      long long c = 0;
+      for (int e = part; e < p.E; e += kGuThreads / 96) {
+        const int g0 = min(l.cum[e], dealt), g1 = min(l.cum[e + 1], dealt);
+        const int n = (g1 + cols - 1 - q) / cols - (g0 + cols - 1 - q) / cols;  // tiles q, q + cols, ... among them
+        c += (long long)n * Tiles::steps(p, l.off[e + 1] - l.off[e]);
       }
+      c *= Tiles::cost(Tiles::padded(Tiles::width(p.n_out, Tiles::count(p.n_out))));
+      atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[q]), (unsigned long long)c);
     }
   }
   // the costs of the tiles that are split (at most kGuTailMost - 1 of them)
@@ -372,9 +434,9 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
       if (i0 + lane < tails) l.tail[i0 + lane] = sum + y - v;
       sum += __shfl_sync(0xffffffffu, y, 31);
     }
-    if (whole == 0) {
+    if (OP != G_DW || whole == 0) {
       // pieces of one length, a tile cut into split_most on average at most
-      const long long pieces = max(1LL, min((long long)cols, (long long)tails * split_most));
+      const int pieces = max(1, (int)min((long long)cols, (long long)tails * split_most));
       for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * sum / pieces : sum;
     } else {
       // a piece brings its pair up to the mean of all pairs
@@ -406,27 +468,45 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
   return n_tiles;
 }
 
-template <typename T>
-MOE_DEV T gu_cast(float v);
-template <>
-MOE_DEV float gu_cast<float>(float v) { return v; }
-template <>
-MOE_DEV __nv_bfloat16 gu_cast<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-MOE_DEV __half gu_cast<__half>(float v) { return __float2half_rn(v); }
-
-// 32 columns (output rows n .. n+31) of this lane's M value
-template <typename T>
-MOE_DEV void gu_store32_t(void* out, long long base, long long ld, int left, const float (&v)[32]) {
-  T* o = reinterpret_cast<T*>(out) + base;
+// Output rows leave through shared memory: a warp has 32 M values (lanes) of up
+// to 16 rows as fp32 words [row][lane] in `buf`, and stores them as 16-byte
+// pieces where the rows allow it (`vec`: all 32 values there, 16-byte aligned
+// rows), else value by value.  `base`: element of the first row's first value.
+MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int rows, int vals, bool vec, uint32_t buf) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (vec && type != G_FP32) {
+    const int v = (lane & 3) * 8;
+#pragma unroll 1
+    for (int r = lane >> 2; r < rows; r += 8) {
+      const uint4 a = tc_lds128(buf + (uint32_t)(r * 128 + v * 4)), b = tc_lds128(buf + (uint32_t)(r * 128 + v * 4 + 16));
+      const float f[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                          __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+      uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < left) o[i * ld] = gu_cast<T>(v[i]);
-}
-MOE_DEV void gu_store32(void* out, int type, long long base, long long ld, int left, const float (&v)[32]) {
-  if (type == G_BF16) gu_store32_t<__nv_bfloat16>(out, base, ld, left, v);
-  else if (type == G_FP16) gu_store32_t<__half>(out, base, ld, left, v);
-  else gu_store32_t<float>(out, base, ld, left, v);
+      for (int i = 0; i < 4; ++i) {
+        if (type == G_BF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + base + r * ld + v) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else if (vec) {
+    const int v = (lane & 7) * 4;
+#pragma unroll 1
+    for (int r = lane >> 3; r < rows; r += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<float*>(out) + base + r * ld + v) =
+          tc_lds128(buf + (uint32_t)(r * 128 + v * 4));
+  } else if (lane < vals) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+      gmm_store(out, type, base + r * ld + lane, __uint_as_float(tc_lds32(buf + (uint32_t)(r * 128 + lane * 4))));
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------ the kernel
@@ -449,7 +529,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   constexpr int kBarSc = 2 * kGuStages + 2 * kGuSegs;
   auto sc_full = [&](int s) { return bar + 8u * (kBarSc + s); };                        // scale warp
   auto sc_empty = [&](int s) { return bar + 8u * (kBarSc + kGuScaleSlots + s); };       // epilogue warps
-  constexpr int kBars = kBarSc + 2 * kGuScaleSlots;
+  constexpr int kBarIt = kBarSc + 2 * kGuScaleSlots;
+  auto it_full = [&](int s) { return bar + 8u * (kBarIt + s); };                        // item warp
+  auto it_empty = [&](int s) { return bar + 8u * (kBarIt + kGuItems + s); };            // this CTA's other warps
+  constexpr int kBars = kBarIt + 2 * kGuItems;
   const uint32_t drain = bar + 8u * kBars;                                              // (L)
   const uint32_t join = drain + 8u;                                                     // epilogue warps
   int* tail = reinterpret_cast<int*>(gen + kGuBarOff + 8 * (kBars + 2));
@@ -479,6 +562,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       tc_bar_init(sc_full(s), 1);
       tc_bar_init(sc_empty(s), kGuEpiWarps);
     }
+    for (int s = 0; s < kGuItems; ++s) {
+      tc_bar_init(it_full(s), 1);
+      tc_bar_init(it_empty(s), 1 + (leader ? 1 : 0) + (FP8 ? 1 : 0) + kGuEpiWarps);
+    }
     tc_bar_init(drain, 1);
     tc_bar_init(join, kGuEpiWarps);
     *abort_flag = 0;
@@ -504,6 +591,21 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The next item; false after the last.  Called by whole warps, or by lane 0
+  // alone (`alone`); lane 0 gives the item's place back.
+  int it_at = 0;
+  uint32_t it_ph = 0;
+  auto next_item = [&](GuItem& it, bool alone) {
+    bool got = tc_bar_wait(it_full(it_at), it_ph, abort_flag);
+    if (!alone) got = __all_sync(0xffffffffu, got) != 0;
+    if (!got) return false;
+    it = line.item[it_at];
+    if (!alone) __syncwarp();
+    if (lane == 0) tc_bar_arrive(it_empty(it_at));
+    if (++it_at == kGuItems) it_at = 0, it_ph ^= 1u;
+    return it.kind != GU_STOP;
+  };
+
   if (warp < 4) {
     // the sums of CHAIN > 0 are the epilogue's registers (the host checks that the block has kGuRegs per thread)
     if constexpr (CHAIN > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
@@ -511,13 +613,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       // ================= TMA issuer of this CTA's halves of both operands
       if (lane == 0) {
         um_prefetch_map(&p.a_map);
-        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
         GuItem it;
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        while (ok && walk.next(it)) {
-          if (it.none) continue;
+        while (ok && next_item(it, true)) {
+          if (it.kind == GU_ZEROS) continue;
           const int half = it.np >> 1;
           const int m = it.m0 + (int)rank * 128;
           const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
@@ -574,7 +675,6 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     } else if (warp == 1) {
       // ================= MMA issuer (leader CTA)
       if (leader && lane == 0) {
-        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
         GuItem it;
         int st = 0, seg = 0;
         uint32_t ph = 0;
@@ -582,21 +682,22 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         GuRing ring;
         int user[kGuSegs];  // the last sum in each TMEM slot
         int done = -1;      // the latest sum known to be through the epilogue
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < kGuSegs; ++i) user[i] = -1;
         const uint32_t idesc0 = (1u << 4) | ((uint32_t)(p.type == G_BF16 ? 1 : 0) * ((1u << 7) | (1u << 10))) |
                                 ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (16u << 24);
         const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + kGuTile, B_MN);
-        while (ok && walk.next(it)) {
-          if (it.none) continue;
+        while (ok && next_item(it, true)) {
+          if (it.kind == GU_ZEROS) continue;
           const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
           for (int kb = it.kb0; kb < it.kb1;) {
-            const int kend = CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
+            const int stride = gu_stride(it.np);  // FP8
+            const int kend = FP8 ? min(it.kb1, kb + kGuN / stride) : CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
             // The sums leave the epilogue in order, so all that used these
             // slots or this barrier (eight sums ago) are through once the
             // latest of them is.  One already seen through is not waited for
             // again: its barrier may be phases ahead.
-            const int at = ring.take(it.np);
+            const int at = ring.take(FP8 ? kGuN : it.np);
             int before = seg - kGuSegs;
 #pragma unroll
             for (int i = 0; i < kGuSegs; ++i)
@@ -612,7 +713,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
               done = before;
             }
             tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)at * kGuSlotCols;
+            uint32_t d = tmem + (uint32_t)at * kGuSlotCols;
             uint32_t acc = 0;
             for (; kb < kend; ++kb) {
               if (!cl_bar_wait(full(st), ph, abort_flag)) {
@@ -623,7 +724,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
               const uint64_t so = (uint64_t)((uint32_t)st * 2 * kGuTile >> 4);
               int steps = 4;
               if constexpr (OP == G_DW) steps = min(4, (it.r1 - it.r0 - kb * KE + 15) >> 4);
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (OP != G_DW || k < steps) {
                   // 16 (e4m3: 32) contracted values: 32 bytes along a K-major row, 16 rows of a panel otherwise
@@ -631,6 +732,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                               db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
                   acc = 1;
                 }
+              if constexpr (FP8) {
+                acc = 0;
+                d += stride;
+              }
               umma2_commit_both(empty(st));
               if (++st == kGuStages) st = 0, ph ^= 1u;
             }
@@ -648,42 +753,43 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     } else if (warp == 2) {
       // ================= 8-bit product: the scales of each step, row scale times this CTA's weight scale
       if constexpr (FP8) {
-        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
         GuItem it;
         int slot = 0;
         uint32_t ph = 0;
         bool ok = true;
         const int groups = (g.n_in + 127) >> 7;
-        constexpr int AHEAD = 4;  // steps whose loads are in flight together
-        while (ok && walk.next(it)) {
+        constexpr int AHEAD = 4;  // hand-overs whose loads are in flight together
+        while (ok && next_item(it, false)) {
           const int ob = (it.m0 >> 7) + (int)rank;
           const float* swp = g.sw + ((long long)it.e * ((g.n_out + 127) >> 7) + ob) * groups;
           const bool live = ob * 128 < g.n_out;
           const float* sxp = g.sx + it.n0;
-          for (int k0 = it.kb0; k0 < it.kb1 && ok; k0 += AHEAD) {
-            float v[AHEAD][8], w[AHEAD];
-  #pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-              const int kb = min(k0 + a, it.kb1 - 1);
-              w[a] = live ? __ldg(swp + kb) : 0.f;
-  #pragma unroll
+          const int stride = gu_stride(it.np), per = kGuN / stride;
+          for (int k0 = it.kb0; k0 < it.kb1 && ok; k0 += AHEAD * per) {
+            float v[AHEAD][8];
+            // (a lane holds the weight scale of one of these at most 16 steps)
+            const float w = live && k0 + lane < it.kb1 && lane < AHEAD * per ? __ldg(swp + k0 + lane) : 0.f;
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const int c = lane + 32 * j;
-                v[a][j] = c < it.nv ? __ldg(sxp + (long long)kb * g.rows + c) : 0.f;
+                const int i = lane + 32 * j, kb = k0 + a * per + i / stride, c = i & (stride - 1);
+                v[a][j] = kb < it.kb1 && c < it.nv ? __ldg(sxp + (long long)kb * g.rows + c) : 0.f;
               }
-            }
-  #pragma unroll
+#pragma unroll
             for (int a = 0; a < AHEAD; ++a) {
-              if (k0 + a >= it.kb1) break;
+              if (k0 + a * per >= it.kb1) break;
               ok = cl_bar_wait(sc_empty(slot), ph ^ 1u, abort_flag);
               if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
               }
               const uint32_t dst = sc0 + (uint32_t)slot * kGuN * 4 + 4u * lane;
-  #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 128u * j), "f"(v[a][j] * w[a]) : "memory");
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float ws = __shfl_sync(0xffffffffu, w, a * per + 32 * j / stride);
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 128u * j), "f"(v[a][j] * ws) : "memory");
+              }
               __syncwarp();
               if (lane == 0) tc_bar_arrive(sc_full(slot));
               if (++slot == kGuScaleSlots) slot = 0, ph ^= 1u;
@@ -691,12 +797,32 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           }
         }
       }
+    } else {
+      // ================= the items of this CTA, a few ahead of the warps that work on them
+      if (lane == 0) {
+        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+        GuItem it;
+        int at = 0;
+        uint32_t ph = 0;
+        for (bool more = true; more;) {
+          more = walk.next(it);
+          if (!more) it.kind = GU_STOP;
+          if (!tc_bar_wait(it_empty(at), ph ^ 1u, abort_flag)) break;
+          line.item[at] = it;
+          tc_bar_arrive(it_full(at));
+          if (++at == kGuItems) at = 0, ph ^= 1u;
+        }
+      }
+      __syncwarp();
     }
   } else {
     if constexpr (CHAIN > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every other 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
-    Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+    const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * kGuStageRows * 128);
+    const long long ld = OP == G_DW ? g.n_in : g.ld_out;
+    const int out_bytes = g.out_type == G_FP32 ? 4 : 2;
+    const bool rows_aligned = ld * out_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
     GuItem it;
     GuRing ring;
     int seg = 0, slot = 0;
@@ -716,15 +842,29 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
              32 * q + lane;
     };
     bool ok = true;
-    while (ok && walk.next(it)) {
+    while (ok && next_item(it, false)) {
       const int chunks = (it.np + 31) >> 5;
-      const int m = it.m0 + (int)rank * 128 + 32 * q + lane;
-      const long long ld = OP == G_DW ? g.n_in : g.ld_out;
+      const int m = it.m0 + (int)rank * 128 + 32 * q;  // the warp's first M value
       const long long ob = (OP == G_DW ? ((long long)it.e * g.n_out + it.n0) * g.n_in : (long long)it.n0 * g.ld_out) + m;
+      const int vals = min(32, m_all - m);
+      const bool vec = rows_aligned && vals == 32;
       const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
+      auto rows_out = [&](int c, const float (&v)[32]) {  // rows 32 c .. of the tile
+        if (vals <= 0) return;
+#pragma unroll
+        for (int u = 0; u < 32; u += kGuStageRows) {
+          const int rows = min(kGuStageRows, it.nv - 32 * c - u);
+          if (rows > 0) {
+#pragma unroll
+            for (int i = 0; i < kGuStageRows; ++i)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[u + i]) : "memory");
+            gu_rows_out(g.out, g.out_type, ob + (32 * c + u) * ld, ld, rows, vals, vec, buf);
+          }
+        }
+      };
       auto put = [&](int c, const float (&v)[32]) {
         if (all) {
-          if (m < m_all) gu_store32(g.out, g.out_type, ob + 32 * c * ld, ld, it.nv - 32 * c, v);
+          rows_out(c, v);
         } else {
           float4* part = part_of((int)pair, it.kb0 > 0 ? 0 : 1) + 8 * c * 128;
 #pragma unroll
@@ -732,12 +872,11 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
             __stcg(part + i * 128, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
       };
-      if (it.none) {
+      if (it.kind == GU_ZEROS) {
         float z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0.f;
-        for (int c = h; c < chunks; c += 2)
-          if (m < m_all) gu_store32(g.out, g.out_type, ob + 32 * c * ld, ld, it.nv - 32 * c, z);
+        for (int c = h; c < chunks; c += 2) rows_out(c, z);
         continue;
       }
       if constexpr (CHAIN == 0) {
@@ -761,44 +900,78 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[j][i] = 0;
-        for (int kb = it.kb0; kb < it.kb1; kb += CHAIN) {
-          const int b = seg & (kGuSegs - 1), at = ring.take(it.np);
-          ok = cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
-          if (FP8) ok = ok && tc_bar_wait(sc_full(slot), sph, abort_flag);
+        // columns 64 j + 32 h of a half belong to this warp's j-th sum (one
+        // step per half), its (j mod 2)-th (two steps), or its only one (four)
+        const int stride = gu_stride(it.np);
+        constexpr int RW = 32;  // columns per TMEM read
+        for (int kb = it.kb0; kb < it.kb1; kb += FP8 ? kGuN / stride : CHAIN) {
+          const int b = seg & (kGuSegs - 1), at = ring.take(FP8 ? kGuN : it.np);
+          if (FP8) ok = tc_bar_wait(sc_full(slot), sph, abort_flag);  // (there before the sums are)
+          ok = ok && cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sp = sc0 + (uint32_t)slot * kGuN * 4;
-          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols);
+          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+          if constexpr (FP8) {
+            const uint32_t sp = sc0 + (uint32_t)(slot * kGuN + 32 * h) * 4;
+            auto give_back = [&]() {  // the half's last values are in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
+            };
+            uint32_t r0[RW], r1[RW];
+            // (columns beyond the tile's rows hold what was there before and are not stored)
+            if (stride == 256) {
+              gu_ld_issue(ta, r0);
+              gu_ld_wait(r0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = 2 * j + h;
-            if (c < chunks) {
-              float v[32];
-              gu_ld32(ta + 32u * c, v);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                if constexpr (FP8) {
-                  const ulonglong2 s = gu_lds_u64x2(sp + (uint32_t)(32 * c + i) * 4);
-                  gu_fma2(acc[j][i / 2], gu_pack(v[i], v[i + 1]), s.x);
-                  gu_fma2(acc[j][i / 2 + 1], gu_pack(v[i + 2], v[i + 3]), s.y);
-                } else {
-                  gu_add2(acc[j][i / 2], gu_pack(v[i], v[i + 1]));
-                  gu_add2(acc[j][i / 2 + 1], gu_pack(v[i + 2], v[i + 3]));
-                }
+              for (int t = 0; t < 128 / RW; t += 2) {
+                constexpr int P = 32 / RW;  // parts of a 32-column range
+                gu_ld_issue(ta + (uint32_t)(64 * ((t + 1) / P) + RW * ((t + 1) % P)), r1);
+                gu_scaled(acc[t / P], RW * (t % P), r0, sp + 4u * (64 * (t / P) + RW * (t % P)));
+                gu_ld_wait(r1);
+                if (t + 2 < 128 / RW) gu_ld_issue(ta + (uint32_t)(64 * ((t + 2) / P) + RW * ((t + 2) % P)), r0);
+                else give_back();
+                gu_scaled(acc[(t + 1) / P], RW * ((t + 1) % P), r1, sp + 4u * (64 * ((t + 1) / P) + RW * ((t + 1) % P)));
+                if (t + 2 < 128 / RW) gu_ld_wait(r0);
               }
+            } else {
+              const int ranges = min(kGuN / stride, it.kb1 - kb) * (stride >> 6);  // 64 columns each, 32 for this warp
+              const int mask = stride == 128 ? 1 : 0;
+              if (32 * h < it.np) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (j < ranges) {
+#pragma unroll
+                    for (int u = 0; u < 32; u += RW) {
+                      gu_ld_issue(ta + (uint32_t)(64 * j + u), r0);
+                      gu_ld_wait(r0);
+                      if (j & mask) gu_scaled(acc[1], u, r0, sp + 4u * (64 * j + u));
+                      else gu_scaled(acc[0], u, r0, sp + 4u * (64 * j + u));
+                    }
+                  }
+              }
+              give_back();
             }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            cl_arrive(cl_addr(acc_empty(b), 0));
-            if (FP8) tc_bar_arrive(sc_empty(slot));
+            __syncwarp();
+            if (lane == 0) tc_bar_arrive(sc_empty(slot));
+            if (++slot == kGuScaleSlots) slot = 0, sph ^= 1u;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (2 * j + h < chunks) {
+                float v[32];
+                gu_ld32(ta + 64u * j, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) gu_add2(acc[j][i], gu_pack(v[2 * i], v[2 * i + 1]));
+              }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
           }
           ++seg;
-          if (FP8 && ++slot == kGuScaleSlots) slot = 0, sph ^= 1u;
         }
         if (!ok) break;
 #pragma unroll
@@ -884,7 +1057,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                   }
                 }
               }
-            if (m < m_all) gu_store32(g.out, g.out_type, ob + 32 * c * ld, ld, it.nv - 32 * c, v);
+            rows_out(c, v);
           }
         }
       }
