@@ -611,26 +611,25 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     if constexpr (CHAIN > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
     if (warp == 0) {
       // ================= TMA issuer of this CTA's halves of both operands
-      if (lane == 0) {
-        um_prefetch_map(&p.a_map);
-        GuItem it;
-        int st = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok && next_item(it, true)) {
-          if (it.kind == GU_ZEROS) continue;
-          const int half = it.np >> 1;
-          const int m = it.m0 + (int)rank * 128;
-          const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-          const int panels = (half + 63) >> 6;  // dw
-          for (int kb = it.kb0; kb < it.kb1; ++kb) {
-            if (!cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            const uint32_t a = base + (uint32_t)st * 2 * kGuTile, b = a + kGuTile;
-            const uint32_t fb = cl_addr(full(st), 0);
-            if constexpr (OP != G_DW) {
+      // (lane 0; all lanes share the many small copies of dw's last steps)
+      if (lane == 0) um_prefetch_map(&p.a_map);
+      GuItem it;
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      while (ok && next_item(it, false)) {
+        if (it.kind == GU_ZEROS) continue;
+        const int half = it.np >> 1;
+        const int m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
+        const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        const int panels = (half + 63) >> 6;  // dw
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
+          if (!ok) break;
+          const uint32_t a = base + (uint32_t)st * 2 * kGuTile, b = a + kGuTile;
+          const uint32_t fb = cl_addr(full(st), 0);
+          if constexpr (OP != G_DW) {
+            if (lane == 0) {
               if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (16 << bx) * 128)));
               if constexpr (OP == G_MM) {
                 gu_tma_3d(a, &p.a_map, kb * KE, m, it.e, fb);
@@ -638,37 +637,43 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                 gu_tma_3d(a, &p.a_map, m, kb * KE, it.e, fb);
                 gu_tma_3d(a + 8192, &p.a_map, m + 64, kb * KE, it.e, fb);
               }
-              gu_tma_2d(b, &p.b_map[bx], kb * KE, it.n0 + (int)rank * half, fb);
-            } else {
-              const int y = it.r0 + kb * KE, left = it.r1 - y, n = it.n0 + (int)rank * half;
-              if (left >= KE) {
+              gu_tma_2d(b, &p.b_map[bx], kb * KE, n, fb);
+            }
+          } else {
+            const int y = it.r0 + kb * KE, left = it.r1 - y;
+            if (left >= KE) {
+              if (lane == 0) {
                 if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + panels * 8192)));
                 gu_tma_2d(a, &p.a_map, m, y, fb);
                 gu_tma_2d(a + 8192, &p.a_map, m + 64, y, fb);
                 for (int q = 0; q < panels; ++q) gu_tma_2d(b + q * 8192, &p.b_map[0], n + 64 * q, y, fb);
-              } else {
-                const int fill = (left + 15) & ~15;
-                if (leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (2 + panels)));
-                for (int q = 0; q < 2 + panels; ++q) {
-                  const bool isa = q < 2;
-                  const uint32_t dst = isa ? a + q * 8192 : b + (q - 2) * 8192;
-                  const int x = isa ? m + 64 * q : n + 64 * (q - 2);
-                  const CUtensorMap* maps = isa ? p.a_tail : p.b_tail;
-                  int r = 0;
-                  for (; r + 8 <= left; r += 8) gu_tma_2d(dst + r * 128, &maps[0], x, y + r, fb);
-                  for (; r & 7 || r < left; ++r)  // rows beyond the expert's: from beyond the tensor, zeros
-                    gu_tma_2d(dst + r * 128, &maps[1], x, r < left ? y + r : g.rows, fb);
-                  if (r < fill) gu_tma_2d(dst + r * 128, &maps[0], x, g.rows, fb);
-                }
               }
+            } else {
+              // Rows up to a multiple of 16: eight at a time while the expert
+              // has eight, then one by one to the next multiple of eight (those
+              // beyond the expert's from beyond the tensor, zeros), then eight
+              // zero rows if the multiple of 16 is not reached.
+              const int fill = (left + 15) & ~15, eights = left >> 3, ones = left & 7 ? 8 : 0;
+              const int zeros = fill - 8 * eights - ones > 0 ? 1 : 0, pieces = eights + ones + zeros;
+              if (lane == 0 && leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (2 + panels)));
+              __syncwarp();
+              for (int i = lane; i < pieces * (2 + panels); i += 32) {
+                const int q = i / pieces, w = i - q * pieces;
+                const bool one = w >= eights && w < eights + ones;
+                const int r = w < eights ? 8 * w : one ? 8 * eights + w - eights : 8 * eights + ones;
+                const uint32_t dst = (q < 2 ? a + q * 8192 : b + (q - 2) * 8192) + (uint32_t)(r * 128);
+                const CUtensorMap* maps = q < 2 ? p.a_tail : p.b_tail;
+                gu_tma_2d(dst, &maps[one ? 1 : 0], q < 2 ? m + 64 * q : n + 64 * (q - 2), r < left ? y + r : g.rows, fb);
+              }
+              __syncwarp();
             }
-            if (++st == kGuStages) st = 0, ph ^= 1u;
           }
+          if (++st == kGuStages) st = 0, ph ^= 1u;
         }
-        if (!ok) {  // a wait gave up: let the copies in flight land before this CTA's memory is released
-          const long long t0 = clock64();
-          while (clock64() - t0 < kGuLinger) {
-          }
+      }
+      if (!ok) {  // a wait gave up: let the copies in flight land before this CTA's memory is released
+        const long long t0 = clock64();
+        while (clock64() - t0 < kGuLinger) {
         }
       }
       __syncwarp();
