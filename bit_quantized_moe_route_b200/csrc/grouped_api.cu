@@ -107,14 +107,14 @@ moe_status_t launch_any(const GmmProblem& p, cudaStream_t s, int sms) {
 }
 
 // Resident pairs of a tensor-memory kernel on the current device (0: none).
-template <int OP, bool FP8, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int CHAIN>
 int resident_pairs() {
   static std::atomic<int> cached[64];  // pairs + 1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = cached[dev].load(std::memory_order_acquire);
   if (!v) {
-    v = gu_pairs<OP, FP8, CHAIN>() + 1;
+    v = gu_pairs<OP, FP8, ROWM, CHAIN>() + 1;
     cached[dev].store(v, std::memory_order_release);
   }
   return v - 1;
@@ -128,14 +128,17 @@ template <int OP>
 bool umma_ok(const GmmProblem& p, int es) {
   if (p.rows < 1 || !aligned16(p.rows_in) || p.ld_rows * es % 16) return false;
   if (OP == G_DW ? !aligned16(p.x) || p.ld_x * es % 16 : !aligned16(p.w) || (long long)p.n_in * es % 16) return false;
-  const long long n = OP == G_DW ? p.n_out : p.rows, m = OP == G_MM ? p.n_out : p.n_in;
+  const long long n = OP == G_DW ? p.n_in : p.rows, m = OP == G_DX ? p.n_in : p.n_out;
   const long long k = OP == G_MM ? p.n_in : OP == G_DX ? p.n_out : p.rows;
-  return (n / kGuN + 1) * (m / 256 + 1) * (k / 64 + 1) < (1LL << 31);
+  return (n / 128 + 1) * (m / 256 + 1) * (k / 64 + 1) < (1LL << 31);
 }
 
-template <int OP, bool FP8, int CHAIN>
+// The 8-bit product has its rows on the M side from this mean per expert on.
+constexpr long long kRowsPerExpertM = 192;
+
+template <int OP, bool FP8, bool ROWM, int CHAIN>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
-  const int pairs = resident_pairs<OP, FP8, CHAIN>();
+  const int pairs = resident_pairs<OP, FP8, ROWM, CHAIN>();
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
   const uint64_t es = FP8 ? 1 : 2;
   const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -152,23 +155,23 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
     const uint32_t rows[3] = {64, 8, 1};
     for (int i = 0; i < 3; ++i) {
       const uint32_t box[2] = {inner, rows[i]};
-      GMM_TRY(api_tensor_map(i ? &q.a_tail[i - 1] : &q.a_map, dt, 2, p.x, dims_x, st_x, box));
-      GMM_TRY(api_tensor_map(i ? &q.b_tail[i - 1] : &q.b_map[0], dt, 2, p.rows_in, dims_y, st_y, box));
+      GMM_TRY(api_tensor_map(i ? &q.a_tail[i - 1] : &q.a_map, dt, 2, p.rows_in, dims_y, st_y, box));
+      GMM_TRY(api_tensor_map(i ? &q.b_tail[i - 1] : &q.b_map[0], dt, 2, p.x, dims_x, st_x, box));
     }
   } else {
     const uint64_t dims_w[3] = {(uint64_t)p.n_in, (uint64_t)p.n_out, (uint64_t)p.E};
     const uint64_t st_w[2] = {(uint64_t)p.n_in * es, (uint64_t)p.n_in * p.n_out * es};
     const uint32_t box_w[3] = {inner, OP == G_MM ? 128u : 64u, 1u};
-    GMM_TRY(api_tensor_map(&q.a_map, dt, 3, p.w, dims_w, st_w, box_w));
+    GMM_TRY(api_tensor_map(ROWM ? &q.b_map[0] : &q.a_map, dt, 3, p.w, dims_w, st_w, box_w));
     const uint64_t dims_r[2] = {(uint64_t)(OP == G_MM ? p.n_in : p.n_out), (uint64_t)p.rows};
     const uint64_t st_r[1] = {(uint64_t)p.ld_rows * es};
     // no tile has more rows than there are: boxes beyond the first that holds half of them are not used
-    for (int i = 0; i < 4 && (i == 0 || p.rows > (32 << (i - 1))); ++i) {
+    for (int i = ROWM ? 3 : 0; i < 4 && (ROWM || i == 0 || p.rows > (32 << (i - 1))); ++i) {
       const uint32_t box[2] = {inner, 16u << i};
-      GMM_TRY(api_tensor_map(&q.b_map[i], dt, 2, p.rows_in, dims_r, st_r, box));
+      GMM_TRY(api_tensor_map(ROWM ? &q.a_map : &q.b_map[i], dt, 2, p.rows_in, dims_r, st_r, box));
     }
   }
-  if (!gu_launch<OP, FP8, CHAIN>(q, pairs, s))
+  if (!gu_launch<OP, FP8, ROWM, CHAIN>(q, pairs, s))
     return api_fail(MOE_ERR_CUDA, "grouped_umma_kernel: %s", cudaGetErrorString(cudaGetLastError()));
   return MOE_OK;
 }
@@ -177,9 +180,11 @@ template <int OP>
 moe_status_t run_gmm(const GmmProblem& p, int in_type, void* ws, cudaStream_t s) {
   if (umma_ok<OP>(p, in_type == G_E4M3 ? 1 : 2)) {
     if constexpr (OP == G_MM)
-      if (in_type == G_E4M3) return launch_umma<OP, true, 1>(p, in_type, ws, s);
-    return p.out_type == G_FP32 ? launch_umma<OP, false, kGuChain>(p, in_type, ws, s)
-                                : launch_umma<OP, false, 0>(p, in_type, ws, s);
+      if (in_type == G_E4M3)
+        return (long long)p.rows >= kRowsPerExpertM * p.E ? launch_umma<OP, true, true, 1>(p, in_type, ws, s)
+                                                          : launch_umma<OP, true, false, 1>(p, in_type, ws, s);
+    return p.out_type == G_FP32 ? launch_umma<OP, false, OP == G_DW, kGuChain>(p, in_type, ws, s)
+                                : launch_umma<OP, false, OP == G_DW, 0>(p, in_type, ws, s);
   }
   int sms = 0;
   if (sm_count(&sms)) return api_fail(MOE_ERR_CUDA, "device query failed");

@@ -1,17 +1,23 @@
 // Grouped products on the 5th-generation tensor cores (sm_100a): TMA loads,
 // tcgen05.mma on pairs of SMs, accumulators in tensor memory.
 //
-// A tile is 256 values of the output's contiguous dimension (M side, 128 per
-// CTA of the pair) by up to 256 output rows (N side): the rows of an expert
-// are cut into equal tiles of at most 256, rounded up to 32, so that an
-// expert with few rows costs a narrow MMA and not a padded tile.  Steps of the
+// A tile is 256 values of the M side (128 per CTA of the pair) by up to 256 of
+// the N side: where that is the rows of an expert, they are cut into equal
+// tiles of at most 256 (8-bit: 128), rounded up to 32, so that an expert with
+// few rows costs a narrow MMA and not a padded tile.  Steps of the
 // contracted dimension are 128 bytes per row: 64 16-bit values or 128 e4m3
 // codes, the block of the 8-bit scales.
 //
-//   op   M side (A operand)                  N side (B operand)
-//   mm   W[e] rows o, K-major                x rows, K-major
-//   dx   W[e] columns i, M-major             dy rows, K-major
-//   dw   x columns i, M-major                dy columns o, N-major
+//   kernel      M side (A operand)         N side (B operand)
+//   mm          W[e] rows o, K-major       x rows, K-major
+//   dx          W[e] columns i, M-major    dy rows, K-major
+//   dw          dy columns o, M-major      x columns i, N-major
+//   mm, ROWM    x rows, K-major            W[e] rows o, K-major
+//
+// With the rows on the M side (ROWM: dw, whose output rows are o, and the 8-bit
+// product of many rows per expert) a thread has one output row, so it stores
+// from its registers and has one row scale; with them on the N side the M side
+// is the output's contiguous dimension.
 //
 // One tile step is 16 KB of A and up to 16 KB of B per CTA in a ring of six.
 // M- and N-major operands are 64-value panels of 64 contracted rows.  For dw
@@ -62,14 +68,19 @@ namespace moe {
 constexpr int kGuStages = 6;
 constexpr int kGuTile = 16384;            // bytes of one operand of one step
 constexpr int kGuN = 256;                 // output rows per tile
-constexpr int kGuThreads = 384;           // warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 epilogue
+// Warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 the epilogue, two for each 32
+// TMEM lanes.  (Sixteen epilogue warps were slower: each barrier wait and
+// shared-memory access takes some 300 clocks beside the MMA's and TMA's own
+// traffic, and twice the warps make twice as many.)
 constexpr int kGuEpiWarps = 8;
-constexpr int kGuRegs = 168;              // registers per thread at launch
-constexpr int kGuRegsLow = 88, kGuRegsHigh = 208;  // CHAIN > 0: warps 0-3, epilogue warps
-static_assert(128 * kGuRegsLow + 256 * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
-constexpr int kGuScaleSlots = 4;
-constexpr int kGuItems = 4;               // items handed out ahead
+constexpr int kGuThreads = 128 + 32 * kGuEpiWarps;
 constexpr int kGuStageRows = 16;          // output rows that a warp stores together
+// CHAIN > 0: registers per thread at launch, and then of warps 0-3 and the epilogue
+constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
+static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
+constexpr int kGuScaleSlots = 6;
+constexpr int kGuScaleAhead = 4;          // slots whose copies are in flight
+constexpr int kGuItems = 4;               // items handed out ahead
 constexpr int kGuSegs = 8;                // sums between the MMA and the epilogue; TMEM slots
 constexpr int kGuSlotCols = 512 / kGuSegs;
 constexpr int kGuPart = 128 * kGuN * 4;   // bytes of one partial tile of one CTA
@@ -93,6 +104,10 @@ struct alignas(64) GuParams {
 };
 
 // ------------------------------------------------------------ PTX wrappers
+// 4-byte copy to shared memory, zero if not `in`
+MOE_DEV void gu_cp4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
 MOE_DEV void gu_tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   um_tma_2d_pair(dst, map, x, y, bar);
 }
@@ -197,16 +212,21 @@ MOE_DEV void gu_scaled(unsigned long long (&acc)[16], const int c0, const uint32
     gu_fma2(acc[(c0 + i) / 2 + 1], gu_pack(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), s.y);
   }
 }
+// 16 step sums times one scale (in both halves of `s`)
+MOE_DEV void gu_times(unsigned long long (&acc)[16], const int c0, const uint32_t (&r)[16], unsigned long long s) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) gu_fma2(acc[(c0 + i) / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
+}
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
 // ------------------------------------------------------------ work items
 // A run of steps of one tile.
 struct alignas(16) GuItem {
-  int e, m0, n0, nv;       // expert, first M value, first output row (dw: first o), rows in use
+  int e, m0, n0, nv;       // expert, first M and N value (rows: of the whole input), N values in use
   int np, kb0, kb1, nkb;   // MMA width, steps, the tile's number of steps
   int cost, r0, r1;        // of one step; dw: the expert's rows
   int kind;                // GuKind
   long long pos;           // where the tile begins on the line
-  long long pad;
+  int mv, pad;             // M values in use
 };
 static_assert(sizeof(GuItem) == 64, "four 16-byte pieces");
 enum GuKind : int {
@@ -237,27 +257,33 @@ constexpr uint32_t kGuBarOff = kGuLineOff + sizeof(GuLine);
 constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
-template <int OP, int KE>
+template <int OP, bool FP8, bool ROWM>
 struct GuTiles {
-  // (dw: whole 64-value panels in both CTAs)
-  static constexpr int kRound = OP == G_DW ? 128 : 32;
-  MOE_DEV static int count(int n) { return (n + kGuN - 1) / kGuN; }
-  MOE_DEV static int m_count(const GmmProblem& p) { return ((OP == G_MM ? p.n_out : p.n_in) + 255) >> 8; }
-  MOE_DEV static int of_expert(const GmmProblem& p, int rows) {
-    return m_count(p) * count(OP == G_DW ? p.n_out : rows);
+  static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
+  static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
+  static constexpr int kRound = OP == G_DW ? 128 : 32;          // (dw: whole 64-value panels in both CTAs)
+  MOE_DEV static int m_all(const GmmProblem& p, int rows) {
+    return OP == G_DX ? p.n_in : OP == G_MM && ROWM ? rows : p.n_out;
   }
+  MOE_DEV static int n_all(const GmmProblem& p, int rows) {
+    return OP == G_DW ? p.n_in : OP == G_MM && ROWM ? p.n_out : rows;
+  }
+  MOE_DEV static int m_count(const GmmProblem& p, int rows) { return (m_all(p, rows) + 255) >> 8; }
+  MOE_DEV static int n_count(int n) { return (n + kMost - 1) / kMost; }
+  MOE_DEV static int of_expert(const GmmProblem& p, int rows) { return m_count(p, rows) * n_count(n_all(p, rows)); }
   MOE_DEV static int steps(const GmmProblem& p, int rows) {
     return OP == G_MM ? (p.n_in + KE - 1) / KE : OP == G_DX ? (p.n_out + KE - 1) / KE : max(1, (rows + KE - 1) / KE);
   }
-  // rows per tile: an expert's rows are cut into nt equal tiles
-  MOE_DEV static int width(int n_all, int nt) {
-    return min(kGuN, (int)(((unsigned)n_all + nt - 1) / (unsigned)nt + kRound - 1) & ~(kRound - 1));
+  // N values per tile: n of them are cut into nt equal tiles (8-bit weight rows: into whole scale blocks)
+  MOE_DEV static int width(int n, int nt) {
+    if (FP8 && ROWM) return kGuN;
+    return min(kMost, (int)(((unsigned)n + nt - 1) / (unsigned)nt + kRound - 1) & ~(kRound - 1));
   }
   MOE_DEV static int padded(int nv) { return max(kRound, (nv + kRound - 1) & ~(kRound - 1)); }
   // A step's cost is its operands' bytes (256 rows of A, np of B), between
   // that of reading weights from HBM (the same for every np) and that of the MMA.
   MOE_DEV static int cost(int np) { return 256 + np; }
-  // tile g whole
+  // Tile g whole.  Neighbouring tiles share weights (mm, dx) or rows of x (dw).
   MOE_DEV static void get(const GmmProblem& p, const GuLine& l, int g, GuItem& it) {
     int lo = 0, hi = p.E;  // cum[lo] <= g < cum[hi]
     while (hi - lo > 1) {
@@ -268,16 +294,21 @@ struct GuTiles {
     it.e = lo;
     it.r0 = l.off[lo];
     it.r1 = l.off[lo + 1];
-    const int n_all = OP == G_DW ? p.n_out : it.r1 - it.r0;
-    const unsigned nt = (unsigned)count(n_all), tile = (unsigned)(g - l.cum[lo]);
-    const int tn = width(n_all, (int)nt);
-    const int t_m = (int)(tile / nt), n_begin = (int)(tile - (unsigned)t_m * nt) * tn;
+    const int rows = it.r1 - it.r0, n = n_all(p, rows), nt = n_count(n), tn = width(n, nt);
+    const unsigned fast = (unsigned)(ROWM ? m_count(p, rows) : nt), tile = (unsigned)(g - l.cum[lo]);
+    const int slow = (int)(tile / fast), quick = (int)(tile - (unsigned)slow * fast);
+    const int t_m = ROWM ? quick : slow, t_n = ROWM ? slow : quick;
     it.m0 = t_m * 256;
-    it.nv = max(0, min(tn, n_all - n_begin));
+    it.mv = m_all(p, rows) - it.m0;
+    it.n0 = t_n * tn;
+    it.nv = max(0, min(tn, n - it.n0));
     it.np = padded(it.nv);
-    it.n0 = OP == G_DW ? n_begin : it.r0 + n_begin;
-    it.nkb = steps(p, it.r1 - it.r0);
-    it.kind = OP == G_DW && it.r1 == it.r0 ? GU_ZEROS : GU_RUN;
+    if (OP != G_DW) {
+      if (ROWM) it.m0 += it.r0;
+      else it.n0 += it.r0;
+    }
+    it.nkb = steps(p, rows);
+    it.kind = OP == G_DW && rows == 0 ? GU_ZEROS : GU_RUN;
     it.cost = cost(it.np);
   }
 };
@@ -293,12 +324,12 @@ struct GuRing {
   }
 };
 
-// 8-bit product: columns per step in a half of tensor memory; the half holds
-// 256 / stride steps.
-MOE_DEV int gu_stride(int np) { return np <= 64 ? 64 : np <= 128 ? 128 : 256; }
+// 8-bit product, rows on the N side: columns per step in a half of tensor
+// memory, which holds 256 / stride steps.
+MOE_DEV int gu_stride(int np) { return np <= 64 ? 64 : 128; }
 
 // Walks a pair's work; every warp that does, and both CTAs of the pair, see the same items.
-template <int OP, int KE>
+template <typename Tiles>
 struct GuWalk {
   const GmmProblem& p;
   const GuLine& l;
@@ -325,7 +356,7 @@ struct GuWalk {
   }
   MOE_DEV bool next(GuItem& it) {
     if (row < whole) {
-      GuTiles<OP, KE>::get(p, l, row * cols + pair, it);
+      Tiles::get(p, l, row * cols + pair, it);
       it.kb0 = 0;
       it.kb1 = it.nkb;
       it.pos = 0;
@@ -336,7 +367,7 @@ struct GuWalk {
       const int t = row - whole;
       if (whole * cols + t >= n_tiles || l.tail[t] >= end) break;
       ++row;
-      GuTiles<OP, KE>::get(p, l, whole * cols + t, it);
+      Tiles::get(p, l, whole * cols + t, it);
       it.pos = l.tail[t];
       it.kb0 = steps_before(begin, it);
       it.kb1 = steps_before(end, it);
@@ -353,19 +384,24 @@ struct GuWalk {
   }
 };
 
-// Fills the plan; called by all threads.  Returns the number of tiles, -1 when
-// the offsets are not valid (they are the caller's, and checked before any is
-// used as an index: 0 <= off[0] <= ... <= off[E] <= rows).
-template <int OP, int KE>
-MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, int* whole_out) {
-  using Tiles = GuTiles<OP, KE>;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kWarps = kGuThreads / 32;
-  for (int e = tid; e <= p.E; e += kGuThreads) l.off[e] = gmm_off(p, e);
-  __syncthreads();
+// Fills the plan; called by NT threads (0 .. NT-1 = tid): the item warp alone,
+// or, for dw, whose tiles differ in length by the experts' rows, the block.
+// Returns the number of tiles, -1 when the offsets are not valid (they are the
+// caller's, and checked before any is used as an index: 0 <= off[0] <= ... <=
+// off[E] <= rows).
+template <int OP, typename Tiles, int NT>
+MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split_most, int* whole_out) {
+  const int warp = tid >> 5, lane = tid & 31;
+  auto sync = [] {
+    if constexpr (NT == 32) __syncwarp();
+    else __syncthreads();
+  };
+#pragma unroll 4
+  for (int e = tid; e <= p.E; e += NT) l.off[e] = gmm_off(p, e);
+  sync();
   int bad = 0;
   const int chunks = (p.E + 31) >> 5;
-  for (int k = warp; k < chunks; k += kWarps) {
+  for (int k = warp; k < chunks; k += NT / 32) {
     const int e = 32 * k + lane;
     int n = 0;
     if (e < p.E) {
@@ -382,7 +418,10 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
     if (e < p.E) l.cum[e] = x - n;
     if (lane == 31) l.chunk[k] = x;
   }
-  if (__syncthreads_or(bad)) return -1;
+  if constexpr (NT == 32) bad = __any_sync(0xffffffffu, bad);
+  else bad = __syncthreads_or(bad);
+  if (bad) return -1;
+  sync();
   int x = lane < chunks ? l.chunk[lane] : 0;  // (at most 32 chunks)
   const int own = x;
 #pragma unroll
@@ -391,36 +430,37 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
     if (lane >= o) x += y;
   }
   const int n_tiles = __shfl_sync(0xffffffffu, x, 31);
-  for (int k = warp; k < chunks; k += kWarps) {
+  for (int k = warp; k < chunks; k += NT / 32) {
     const int before = __shfl_sync(0xffffffffu, x - own, k);
-    if (32 * k + lane < p.E) l.cum[32 * k + lane] += before;
+    if (k > 0 && 32 * k + lane < p.E) l.cum[32 * k + lane] += before;
   }
   if (tid == 0) l.cum[p.E] = n_tiles;
   const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = n_tiles - dealt;
-  for (int i = tid; i < cols; i += kGuThreads) l.hand[i] = 0;
-  __syncthreads();
+  if constexpr (OP == G_DW)
+    for (int i = tid; i < cols; i += NT) l.hand[i] = 0;
+  sync();
   // What each pair's whole tiles cost.  mm, dx: as good as the same for all
   // pairs.  dw: a tile's steps are its expert's rows.
-  if (OP == G_DW && whole > 0) {
+  if constexpr (OP == G_DW) {
     const int q = tid % 96, part = tid / 96;
-    if (q < cols) {
+    if (whole > 0 && q < cols) {
       long long c = 0;
-      for (int e = part; e < p.E; e += kGuThreads / 96) {
+      for (int e = part; e < p.E; e += NT / 96) {
         const int g0 = min(l.cum[e], dealt), g1 = min(l.cum[e + 1], dealt);
         const int n = (g1 + cols - 1 - q) / cols - (g0 + cols - 1 - q) / cols;  // tiles q, q + cols, ... among them
         c += (long long)n * Tiles::steps(p, l.off[e + 1] - l.off[e]);
       }
-      c *= Tiles::cost(Tiles::padded(Tiles::width(p.n_out, Tiles::count(p.n_out))));
+      c *= Tiles::cost(Tiles::padded(Tiles::width(p.n_in, Tiles::n_count(p.n_in))));
       atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[q]), (unsigned long long)c);
     }
   }
   // the costs of the tiles that are split (at most kGuTailMost - 1 of them)
-  if (tid < tails) {
+  for (int i = tid; i < tails; i += NT) {
     GuItem it;
-    Tiles::get(p, l, dealt + tid, it);
-    l.tail[tid] = (long long)it.nkb * it.cost;
+    Tiles::get(p, l, dealt + i, it);
+    l.tail[i] = (long long)it.nkb * it.cost;
   }
-  __syncthreads();
+  sync();
   if (warp == 0) {
     long long sum = 0;
     for (int i0 = 0; i0 < tails; i0 += 32) {
@@ -435,9 +475,16 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
       sum += __shfl_sync(0xffffffffu, y, 31);
     }
     if (OP != G_DW || whole == 0) {
-      // pieces of one length, a tile cut into split_most on average at most
-      const int pieces = max(1, (int)min((long long)cols, (long long)tails * split_most));
-      for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * sum / pieces : sum;
+      // Pieces of one length, a tile cut into split_most on average at most.
+      // Fewer tiles than pairs: a whole number of pieces per tile, so that a
+      // pair works on one tile, unless that leaves over a fifth of the pairs
+      // without work (one token over eight experts: 64 tiles whole, no sums
+      // to join, 128 SMs fill the memory's bandwidth as well as 148).
+      int pieces = max(1, (int)min((long long)cols, (long long)tails * split_most));
+      if (tails > 0 && tails < pieces && pieces / tails * tails * 5 >= pieces * 4) pieces = pieces / tails * tails;
+      const long long each = sum / pieces;
+      const int rest = (int)(sum - each * pieces);
+      for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * each + i * rest / pieces : sum;
     } else {
       // a piece brings its pair up to the mean of all pairs
       long long hands = 0;
@@ -464,43 +511,61 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int cols, int split_most, in
     }
     if (lane == 0) l.tail[tails] = sum;
   }
+  sync();
   *whole_out = whole;
   return n_tiles;
 }
 
-// Output rows leave through shared memory: a warp has 32 M values (lanes) of up
-// to 16 rows as fp32 words [row][lane] in `buf`, and stores them as 16-byte
-// pieces where the rows allow it (`vec`: all 32 values there, 16-byte aligned
-// rows), else value by value.  `base`: element of the first row's first value.
+// eight values as 16-bit pairs
+MOE_DEV uint4 gu_pack8(int type, const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == G_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows on the N side leave through shared memory: a warp has 32 M values
+// (lanes) of up to 16 rows as fp32 words [row][lane] in `buf`, and stores them
+// as 16-byte pieces where the rows allow it (`vec`: all 32 values there, 16-byte
+// aligned rows), else value by value.  `base`: element of the first row's first
+// value.
 MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int rows, int vals, bool vec, uint32_t buf) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
   if (vec && type != G_FP32) {
     const int v = (lane & 3) * 8;
-#pragma unroll 1
-    for (int r = lane >> 2; r < rows; r += 8) {
-      const uint4 a = tc_lds128(buf + (uint32_t)(r * 128 + v * 4)), b = tc_lds128(buf + (uint32_t)(r * 128 + v * 4 + 16));
-      const float f[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
-                          __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
-      uint32_t w[4];
+    float f[2][8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (type == G_BF16) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const uint4 a = tc_lds128(buf + (uint32_t)(((lane >> 2) + 8 * k) * 128 + (v + i) * 4));
+        f[k][i] = __uint_as_float(a.x);
+        f[k][i + 1] = __uint_as_float(a.y);
+        f[k][i + 2] = __uint_as_float(a.z);
+        f[k][i + 3] = __uint_as_float(a.w);
       }
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + base + r * ld + v) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = (lane >> 2) + 8 * k;
+      if (r < rows)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + base + r * ld + v) = gu_pack8(type, f[k]);
     }
   } else if (vec) {
     const int v = (lane & 7) * 4;
-#pragma unroll 1
-    for (int r = lane >> 3; r < rows; r += 4)
-      *reinterpret_cast<uint4*>(reinterpret_cast<float*>(out) + base + r * ld + v) =
-          tc_lds128(buf + (uint32_t)(r * 128 + v * 4));
+#pragma unroll
+    for (int r = lane >> 3; r < kGuStageRows; r += 4)
+      if (r < rows)
+        *reinterpret_cast<uint4*>(reinterpret_cast<float*>(out) + base + r * ld + v) =
+            tc_lds128(buf + (uint32_t)(r * 128 + v * 4));
   } else if (lane < vals) {
 #pragma unroll 1
     for (int r = 0; r < rows; ++r)
@@ -509,12 +574,38 @@ MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int 
   __syncwarp();
 }
 
+// Rows on the M side: W values of this lane's row, from element `base` on, of
+// which `left` are there; `vec`: 16-byte aligned rows.
+template <int W>
+MOE_DEV void gu_row_out(void* out, int type, long long base, int left, bool vec, const float* v) {
+  if (vec && left >= W) {
+    if (type == G_FP32) {
+      float* o = reinterpret_cast<float*>(out) + base;
+#pragma unroll
+      for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+      uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
+#pragma unroll
+      for (int i = 0; i < W; i += 8) *reinterpret_cast<uint4*>(o + i) = gu_pack8(type, v + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < left) gmm_store(out, type, base + i, v[i]);
+  }
+}
+
 // ------------------------------------------------------------ the kernel
 // Launched in clusters of two CTAs (gridDim.x even), one CTA per SM.
-template <int OP, bool FP8, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int CHAIN>
 __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __grid_constant__ GuParams p) {
+  constexpr int EW = kGuEpiWarps, H = EW / 4, SR = kGuStageRows;
+  constexpr bool SCALE_RING = FP8 && !ROWM;  // the scales come through shared memory
+  static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
+  using Tiles = GuTiles<OP, FP8, ROWM>;
+  using Walk = GuWalk<Tiles>;
   constexpr bool A_MN = OP != G_MM, B_MN = OP == G_DW;
-  constexpr int KE = FP8 ? 128 : 64;  // contracted values per step
+  constexpr int KE = Tiles::KE;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw32 = tc_smem(smem_raw);
   const uint32_t base = (raw32 + 1023u) & ~1023u;
@@ -539,7 +630,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = tail + 1;
   int* last_flag = tail + 2;
-  static_assert(8 * (kBars + 2) + 12 <= 512, "barrier block");
+  static_assert(8 * (kBars + 2) + 16 <= 512, "barrier block");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, pair, npairs;
@@ -556,18 +647,18 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     }
     for (int b = 0; b < kGuSegs; ++b) {
       tc_bar_init(acc_full(b), 1);
-      tc_bar_init(acc_empty(b), 2 * kGuEpiWarps);
+      tc_bar_init(acc_empty(b), 2 * EW);
     }
     for (int s = 0; s < kGuScaleSlots; ++s) {
       tc_bar_init(sc_full(s), 1);
-      tc_bar_init(sc_empty(s), kGuEpiWarps);
+      tc_bar_init(sc_empty(s), EW);
     }
     for (int s = 0; s < kGuItems; ++s) {
       tc_bar_init(it_full(s), 1);
-      tc_bar_init(it_empty(s), 1 + (leader ? 1 : 0) + (FP8 ? 1 : 0) + kGuEpiWarps);
+      tc_bar_init(it_empty(s), 1 + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
     }
     tc_bar_init(drain, 1);
-    tc_bar_init(join, kGuEpiWarps);
+    tc_bar_init(join, EW);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -577,33 +668,46 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  using Walk = GuWalk<OP, KE>;
-  const int m_all = OP == G_MM ? g.n_out : g.n_in;
   const int cols = (int)npairs;
-  int whole = 0;
-  const int planned = gu_plan<OP, KE>(g, line, cols, p.split_most, &whole);
-  if (planned < 0 && tid == 0) set_error(g.err, kErrDeviceInput);
-  const int n_tiles = max(planned, 0);
+  // The plan.  Only the item warp works from it (and the epilogue reads the
+  // cuts, after an item), so it makes it while the others set up, but for dw.
+  int whole = 0, n_tiles = -1;
+  if constexpr (OP == G_DW) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole);
   tc_fence_before();
-  __syncthreads();
-  if (planned < 0 && tid < 2) line.cut[pair + tid] = 0;
-  cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated before any cross-CTA use
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (OP != G_DW)
+    if (warp == 3) n_tiles = gu_plan<OP, Tiles, 32>(g, line, lane, cols, p.split_most, &whole);
+  if (warp == 3 && lane == 0 && n_tiles < 0) {
+    set_error(g.err, kErrDeviceInput);
+    line.cut[pair] = line.cut[pair + 1] = 0;
+  }
+  // both CTAs' barriers initialised and TMEM allocated before any cross-CTA use
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // The next item; false after the last.  Called by whole warps, or by lane 0
-  // alone (`alone`); lane 0 gives the item's place back.
+  // The next item, in shared memory until it is given back; NULL after the
+  // last.  Called by whole warps, or by lane 0 alone (`alone`).
   int it_at = 0;
   uint32_t it_ph = 0;
-  auto next_item = [&](GuItem& it, bool alone) {
+  auto next_item = [&](bool alone) -> const GuItem* {
     bool got = tc_bar_wait(it_full(it_at), it_ph, abort_flag);
     if (!alone) got = __all_sync(0xffffffffu, got) != 0;
-    if (!got) return false;
-    it = line.item[it_at];
+    if (!got) return nullptr;
+    const GuItem* it = &line.item[it_at];
+    return it->kind == GU_STOP ? nullptr : it;
+  };
+  auto give_item = [&](bool alone) {
     if (!alone) __syncwarp();
     if (lane == 0) tc_bar_arrive(it_empty(it_at));
     if (++it_at == kGuItems) it_at = 0, it_ph ^= 1u;
-    return it.kind != GU_STOP;
+  };
+  auto copy_item = [&](GuItem& it, bool alone) {
+    const GuItem* src = next_item(alone);
+    if (!src) return false;
+    it = *src;
+    give_item(alone);
+    return true;
   };
 
   if (warp < 4) {
@@ -617,7 +721,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
-      while (ok && next_item(it, false)) {
+      while (ok && copy_item(it, false)) {
         if (it.kind == GU_ZEROS) continue;
         const int half = it.np >> 1;
         const int m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
@@ -630,14 +734,17 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           const uint32_t fb = cl_addr(full(st), 0);
           if constexpr (OP != G_DW) {
             if (lane == 0) {
-              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (16 << bx) * 128)));
-              if constexpr (OP == G_MM) {
+              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (ROWM ? kGuTile : (16 << bx) * 128))));
+              if constexpr (ROWM) {
+                gu_tma_2d(a, &p.a_map, kb * KE, m, fb);
+                gu_tma_3d(b, &p.b_map[0], kb * KE, n, it.e, fb);
+              } else if constexpr (OP == G_MM) {
                 gu_tma_3d(a, &p.a_map, kb * KE, m, it.e, fb);
               } else {
                 gu_tma_3d(a, &p.a_map, m, kb * KE, it.e, fb);
                 gu_tma_3d(a + 8192, &p.a_map, m + 64, kb * KE, it.e, fb);
               }
-              gu_tma_2d(b, &p.b_map[bx], kb * KE, n, fb);
+              if constexpr (!ROWM) gu_tma_2d(b, &p.b_map[bx], kb * KE, n, fb);
             }
           } else {
             const int y = it.r0 + kb * KE, left = it.r1 - y;
@@ -692,12 +799,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         const uint32_t idesc0 = (1u << 4) | ((uint32_t)(p.type == G_BF16 ? 1 : 0) * ((1u << 7) | (1u << 10))) |
                                 ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (16u << 24);
         const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + kGuTile, B_MN);
-        while (ok && next_item(it, true)) {
+        while (ok && copy_item(it, true)) {
           if (it.kind == GU_ZEROS) continue;
           const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
           for (int kb = it.kb0; kb < it.kb1;) {
-            const int stride = gu_stride(it.np);  // FP8
-            const int kend = FP8 ? min(it.kb1, kb + kGuN / stride) : CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
+            const int stride = SCALE_RING ? gu_stride(it.np) : kGuN;
+            const int kend = SCALE_RING ? min(it.kb1, kb + kGuN / stride) : CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
             // The sums leave the epilogue in order, so all that used these
             // slots or this barrier (eight sums ago) are through once the
             // latest of them is.  One already seen through is not waited for
@@ -737,7 +844,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                               db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
                   acc = 1;
                 }
-              if constexpr (FP8) {
+              if constexpr (SCALE_RING) {
                 acc = 0;
                 d += stride;
               }
@@ -756,56 +863,60 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ================= 8-bit product: the scales of each step, row scale times this CTA's weight scale
-      if constexpr (FP8) {
+      // ================= 8-bit product: the scales of each hand-over, row
+      // scale times this CTA's weight scale.  The row scales are copied to
+      // their slot up to kGuScaleAhead slots ahead; each lane then multiplies
+      // those that it copied.
+      if constexpr (SCALE_RING) {
         GuItem it;
-        int slot = 0;
+        int fill = 0, slot = 0;  // the next slot to copy to, and to multiply
+        float w = 0.f;           // this lane's of the weight scales of 32 steps
         uint32_t ph = 0;
         bool ok = true;
         const int groups = (g.n_in + 127) >> 7;
-        constexpr int AHEAD = 4;  // hand-overs whose loads are in flight together
-        while (ok && next_item(it, false)) {
+        while (ok && copy_item(it, false)) {
           const int ob = (it.m0 >> 7) + (int)rank;
           const float* swp = g.sw + ((long long)it.e * ((g.n_out + 127) >> 7) + ob) * groups;
           const bool live = ob * 128 < g.n_out;
-          const float* sxp = g.sx + it.n0;
-          const int stride = gu_stride(it.np), per = kGuN / stride;
-          for (int k0 = it.kb0; k0 < it.kb1 && ok; k0 += AHEAD * per) {
-            float v[AHEAD][8];
-            // (a lane holds the weight scale of one of these at most 16 steps)
-            const float w = live && k0 + lane < it.kb1 && lane < AHEAD * per ? __ldg(swp + k0 + lane) : 0.f;
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int i = lane + 32 * j, kb = k0 + a * per + i / stride, c = i & (stride - 1);
-                v[a][j] = kb < it.kb1 && c < it.nv ? __ldg(sxp + (long long)kb * g.rows + c) : 0.f;
-              }
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-              if (k0 + a * per >= it.kb1) break;
-              ok = cl_bar_wait(sc_empty(slot), ph ^ 1u, abort_flag);
-              if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-              }
-              const uint32_t dst = sc0 + (uint32_t)slot * kGuN * 4 + 4u * lane;
+          const int lg = it.np <= 64 ? 6 : 7, per = kGuN >> lg;  // (gu_stride)
+          const int overs = (it.kb1 - it.kb0 + per - 1) >> (8 - lg);
+          for (int i = 0; i < overs + kGuScaleAhead; ++i) {
+            if (i < overs) {
+              ok = __all_sync(0xffffffffu, cl_bar_wait(sc_empty(fill), ph ^ 1u, abort_flag)) != 0;
+              if (!ok) break;
+              const int k0 = it.kb0 + i * per;
+              const uint32_t dst = sc0 + (uint32_t)(fill * kGuN + lane) * 4;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float ws = __shfl_sync(0xffffffffu, w, a * per + 32 * j / stride);
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 128u * j), "f"(v[a][j] * ws) : "memory");
+                const int kb = k0 + (32 * j >> lg), c = (32 * j + lane) & ((1 << lg) - 1);
+                const bool in = kb < it.kb1 && c < it.nv;
+                gu_cp4(dst + 128u * j, g.sx + (in ? (long long)kb * g.rows + it.n0 + c : 0), in);
               }
-              __syncwarp();
-              if (lane == 0) tc_bar_arrive(sc_full(slot));
-              if (++slot == kGuScaleSlots) slot = 0, ph ^= 1u;
+              if (++fill == kGuScaleSlots) fill = 0, ph ^= 1u;
             }
+            cp_commit();
+            if (i < kGuScaleAhead) continue;
+            const int step = (i - kGuScaleAhead) * per;
+            if ((step & 31) == 0) w = live && it.kb0 + step + lane < it.kb1 ? __ldg(swp + it.kb0 + step + lane) : 0.f;
+            cp_wait<kGuScaleAhead>();
+            const uint32_t at = sc0 + (uint32_t)(slot * kGuN + lane) * 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float ws = __shfl_sync(0xffffffffu, w, (step & 31) + (32 * j >> lg));
+              const float v = __uint_as_float(tc_lds32(at + 128u * j)) * ws;
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128u * j), "f"(v) : "memory");
+            }
+            __syncwarp();
+            if (lane == 0) tc_bar_arrive(sc_full(slot));
+            if (++slot == kGuScaleSlots) slot = 0;
           }
         }
+        cp_wait<0>();
       }
     } else {
       // ================= the items of this CTA, a few ahead of the warps that work on them
       if (lane == 0) {
-        Walk walk(g, line, (int)pair, cols, n_tiles, whole);
+        Walk walk(g, line, (int)pair, cols, max(n_tiles, 0), whole);
         GuItem it;
         int at = 0;
         uint32_t ph = 0;
@@ -822,15 +933,14 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     }
   } else {
     if constexpr (CHAIN > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
-    // ================= epilogue: 32 TMEM lanes (M values) and every other 32 columns (output rows) per warp
+    // ================= epilogue: 32 TMEM lanes (M values) and every H-th 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
-    const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * kGuStageRows * 128);
+    const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * SR * 128);
     const long long ld = OP == G_DW ? g.n_in : g.ld_out;
     const int out_bytes = g.out_type == G_FP32 ? 4 : 2;
     const bool rows_aligned = ld * out_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
-    GuItem it;
     GuRing ring;
-    int seg = 0, slot = 0;
+    int seg = 0, slot = 0, joins = 0;
     uint32_t sph = 0, jph = 0;
     auto epi_sync = [&]() {  // the epilogue warps meet (bounded, unlike a hardware barrier)
       __syncwarp();
@@ -847,29 +957,35 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
              32 * q + lane;
     };
     bool ok = true;
-    while (ok && next_item(it, false)) {
+    while (ok) {
+      GuItem it;
+      if (!copy_item(it, false)) break;
       const int chunks = (it.np + 31) >> 5;
-      const int m = it.m0 + (int)rank * 128 + 32 * q;  // the warp's first M value
-      const long long ob = (OP == G_DW ? ((long long)it.e * g.n_out + it.n0) * g.n_in : (long long)it.n0 * g.ld_out) + m;
-      const int vals = min(32, m_all - m);
-      const bool vec = rows_aligned && vals == 32;
       const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
-      auto rows_out = [&](int c, const float (&v)[32]) {  // rows 32 c .. of the tile
-        if (vals <= 0) return;
+      const int m = (int)rank * 128 + 32 * q;       // the warp's first M value in the tile
+      const int vals = min(32, it.mv - m);          // how many it has
+      const bool vec = rows_aligned && (ROWM || vals == 32);
+      // the first M and N value's output element (rows on the M side: this lane's row)
+      const long long ob =
+          ROWM ? (OP == G_DW ? (long long)it.e * g.n_out + it.m0 + m + lane : (long long)it.m0 + m + lane) * ld + it.n0
+               : (long long)it.n0 * ld + it.m0 + m;
+      // N values SR c .. of the tile, from v[at] on
+      auto out_sr = [&](int c, const auto& v, const int at) {
+        const int left = it.nv - SR * c;
+        if (left <= 0 || vals <= 0) return;
+        if constexpr (ROWM) {
+          if (lane < vals) gu_row_out<SR>(g.out, g.out_type, ob + SR * c, left, vec, &v[at]);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 32; u += kGuStageRows) {
-          const int rows = min(kGuStageRows, it.nv - 32 * c - u);
-          if (rows > 0) {
-#pragma unroll
-            for (int i = 0; i < kGuStageRows; ++i)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[u + i]) : "memory");
-            gu_rows_out(g.out, g.out_type, ob + (32 * c + u) * ld, ld, rows, vals, vec, buf);
-          }
+          for (int i = 0; i < SR; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[at + i]) : "memory");
+          gu_rows_out(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, vec, buf);
         }
       };
-      auto put = [&](int c, const float (&v)[32]) {
+      auto put = [&](int c, const float (&v)[32]) {  // N values 32 c ..
         if (all) {
-          rows_out(c, v);
+          out_sr(2 * c, v, 0);
+          out_sr(2 * c + 1, v, 16);
         } else {
           float4* part = part_of((int)pair, it.kb0 > 0 ? 0 : 1) + 8 * c * 128;
 #pragma unroll
@@ -881,111 +997,135 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         float z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0.f;
-        for (int c = h; c < chunks; c += 2) rows_out(c, z);
+        for (int c = h; c < chunks; c += H) put(c, z);
         continue;
       }
-      if constexpr (CHAIN == 0) {
-        const int b = seg & (kGuSegs - 1), at = ring.take(it.np);
-        ok = cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
+      auto wait_sums = [&]() {
+        const bool got = cl_bar_wait(acc_full(seg & (kGuSegs - 1)), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) return false;
         tc_fence_after();
-        for (int c = h; c < chunks; c += 2) {
+        return true;
+      };
+      auto give_back = [&]() {  // the sums are in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cl_arrive(cl_addr(acc_empty(seg & (kGuSegs - 1)), 0));
+      };
+      if constexpr (CHAIN == 0) {
+        const int at = ring.take(it.np);
+        ok = wait_sums();
+        if (!ok) break;
+        for (int c = h; c < chunks; c += H) {
           float v[32];
           gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
           put(c, v);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
+        give_back();
         ++seg;
       } else {
         // sums in pairs of columns, for the packed fp32 instructions
-        unsigned long long acc[4][16];
+        constexpr int NJ = Tiles::kMost / 64;
+        unsigned long long acc[NJ][16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[j][i] = 0;
-        // columns 64 j + 32 h of a half belong to this warp's j-th sum (one
-        // step per half), its (j mod 2)-th (two steps), or its only one (four)
-        const int stride = gu_stride(it.np);
-        constexpr int RW = 32;  // columns per TMEM read
-        for (int kb = it.kb0; kb < it.kb1; kb += FP8 ? kGuN / stride : CHAIN) {
-          const int b = seg & (kGuSegs - 1), at = ring.take(FP8 ? kGuN : it.np);
-          if (FP8) ok = tc_bar_wait(sc_full(slot), sph, abort_flag);  // (there before the sums are)
-          ok = ok && cl_bar_wait(acc_full(b), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
-          if constexpr (FP8) {
+        if constexpr (SCALE_RING) {
+          const int stride = gu_stride(it.np);
+          for (int kb = it.kb0; kb < it.kb1; kb += kGuN / stride) {
+            const int at = ring.take(kGuN);
+            ok = tc_bar_wait(sc_full(slot), sph, abort_flag);  // (there before the sums are)
+            ok = __all_sync(0xffffffffu, ok) && wait_sums();
+            if (!ok) break;
+            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
             const uint32_t sp = sc0 + (uint32_t)(slot * kGuN + 32 * h) * 4;
-            auto give_back = [&]() {  // the half's last values are in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
-            };
-            uint32_t r0[RW], r1[RW];
-            // (columns beyond the tile's rows hold what was there before and are not stored)
-            if (stride == 256) {
-              gu_ld_issue(ta, r0);
-              gu_ld_wait(r0);
+            const int ranges = min(kGuN / stride, it.kb1 - kb) * (stride >> 6);  // 64 columns each, 32 for this warp
+            if (32 * h < it.np) {
 #pragma unroll
-              for (int t = 0; t < 128 / RW; t += 2) {
-                constexpr int P = 32 / RW;  // parts of a 32-column range
-                gu_ld_issue(ta + (uint32_t)(64 * ((t + 1) / P) + RW * ((t + 1) % P)), r1);
-                gu_scaled(acc[t / P], RW * (t % P), r0, sp + 4u * (64 * (t / P) + RW * (t % P)));
-                gu_ld_wait(r1);
-                if (t + 2 < 128 / RW) gu_ld_issue(ta + (uint32_t)(64 * ((t + 2) / P) + RW * ((t + 2) % P)), r0);
-                else give_back();
-                gu_scaled(acc[(t + 1) / P], RW * ((t + 1) % P), r1, sp + 4u * (64 * ((t + 1) / P) + RW * ((t + 1) % P)));
-                if (t + 2 < 128 / RW) gu_ld_wait(r0);
-              }
-            } else {
-              const int ranges = min(kGuN / stride, it.kb1 - kb) * (stride >> 6);  // 64 columns each, 32 for this warp
-              const int mask = stride == 128 ? 1 : 0;
-              if (32 * h < it.np) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j < ranges) {
-#pragma unroll
-                    for (int u = 0; u < 32; u += RW) {
-                      gu_ld_issue(ta + (uint32_t)(64 * j + u), r0);
-                      gu_ld_wait(r0);
-                      if (j & mask) gu_scaled(acc[1], u, r0, sp + 4u * (64 * j + u));
-                      else gu_scaled(acc[0], u, r0, sp + 4u * (64 * j + u));
-                    }
-                  }
-              }
-              give_back();
+              for (int j = 0; j < 4; ++j)
+                if (j < ranges) {
+                  uint32_t r[32];
+                  gu_ld_issue(ta + 64u * j, r);
+                  gu_ld_wait(r);
+                  if (stride == 128 && (j & 1)) gu_scaled(acc[1], 0, r, sp + 256u * j);
+                  else gu_scaled(acc[0], 0, r, sp + 256u * j);
+                }
             }
-            __syncwarp();
+            give_back();
             if (lane == 0) tc_bar_arrive(sc_empty(slot));
             if (++slot == kGuScaleSlots) slot = 0, sph ^= 1u;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (2 * j + h < chunks) {
-                float v[32];
-                gu_ld32(ta + 64u * j, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) gu_add2(acc[j][i], gu_pack(v[2 * i], v[2 * i + 1]));
-              }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) cl_arrive(cl_addr(acc_empty(b), 0));
+            ++seg;
           }
-          ++seg;
+        } else if constexpr (FP8) {
+          // one row scale per thread and step, one weight scale per half of
+          // the columns; those of the next steps are on their way
+          const int groups = (g.n_in + 127) >> 7, blocks = (g.n_out + 127) >> 7;
+          const float* sxp = g.sx + it.m0 + m + min(lane, max(vals - 1, 0));
+          const float* swp = g.sw + ((long long)it.e * blocks + (it.n0 >> 7)) * groups;
+          const int second = (it.n0 >> 7) + 1 < blocks ? groups : 0;
+          auto scale_of = [&](int kb, float& x, float& a, float& b) {
+            kb = min(kb, it.kb1 - 1);
+            x = vals > 0 ? __ldg(sxp + (long long)kb * g.rows) : 0.f;
+            a = __ldg(swp + kb);
+            b = __ldg(swp + second + kb);
+          };
+          float x0, a0, b0, x1, a1, b1;
+          scale_of(it.kb0, x0, a0, b0);
+          scale_of(it.kb0 + 1, x1, a1, b1);
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            const int at = ring.take(kGuN);
+            const float sa = x0 * a0, sb = x0 * b0;
+            const unsigned long long s0 = gu_pack(sa, sa), s1 = gu_pack(sb, sb);
+            x0 = x1, a0 = a1, b0 = b1;
+            scale_of(kb + 2, x1, a1, b1);
+            ok = wait_sums();
+            if (!ok) break;
+            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+            // columns 64 j + 32 h, j = 0..3, half of them at a time (those
+            // beyond the tile's hold what was there before and are not stored)
+            uint32_t r0[16], r1[16];
+            gu_ld_issue(ta, r0);
+            gu_ld_wait(r0);
+#pragma unroll
+            for (int t = 0; t < 8; t += 2) {
+              gu_ld_issue(ta + (uint32_t)(64 * (t / 2) + 16), r1);
+              gu_times(acc[t / 2], 0, r0, t < 4 ? s0 : s1);
+              gu_ld_wait(r1);
+              if (t < 6) gu_ld_issue(ta + (uint32_t)(64 * (t / 2 + 1)), r0);
+              else give_back();
+              gu_times(acc[t / 2], 16, r1, t < 4 ? s0 : s1);
+              if (t < 6) gu_ld_wait(r0);
+            }
+            ++seg;
+          }
+        } else {
+          for (int kb = it.kb0; kb < it.kb1; kb += CHAIN) {
+            const int at = ring.take(it.np);
+            ok = wait_sums();
+            if (!ok) break;
+            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              if (H * j + h < chunks) {
+                uint32_t r[32];
+                gu_ld_issue(ta + 64u * j, r);
+                gu_ld_wait(r);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                  gu_add2(acc[j][i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+              }
+            give_back();
+            ++seg;
+          }
         }
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (2 * j + h < chunks) {
+        for (int j = 0; j < NJ; ++j)
+          if (H * j + h < chunks) {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 16; ++i) gu_unpack(acc[j][i], v[2 * i], v[2 * i + 1]);
-            put(2 * j + h, v);
+            put(H * j + h, v);
           }
       }
       if (!all) {
@@ -1003,66 +1143,62 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
           return lo;
         };
         const int first = piece_at(it.pos), last = piece_at(it.pos + (long long)(it.nkb - 1) * it.cost);
-        uint32_t has[3] = {0, 0, 0};
+        // of 32 pieces from `from` on, those with a part
+        auto with_part = [&](int from) {
+          const int s = from + lane;
+          return __ballot_sync(0xffffffffu, s <= last && Walk::steps_before(line.cut[s], it) <
+                                                              Walk::steps_before(line.cut[s + 1], it));
+        };
         int parts = 0;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int s = first + 32 * k + lane;
-          const bool in = s <= last && Walk::steps_before(line.cut[s], it) < Walk::steps_before(line.cut[s + 1], it);
-          has[k] = __ballot_sync(0xffffffffu, in);
-          parts += __popc(has[k]);
-        }
+#pragma unroll 1
+        for (int from = first; from <= last; from += 32) parts += __popc(with_part(from));
         __threadfence();
         ok = epi_sync();
         if (!ok) break;
+        volatile int* flag = last_flag + (joins++ & 1);  // (two: the next join's is not this one's)
         if (tid == 128) {
           unsigned* ctr = counters + first * 2 + rank;
           const unsigned before = atomicAdd(ctr, 1u);
-          *last_flag = before + 1 == (unsigned)parts;
+          *flag = before + 1 == (unsigned)parts;
           if (before + 1 == (unsigned)parts) *ctr = 0;
         }
         ok = epi_sync();
         if (!ok) break;
-        const bool mine = *reinterpret_cast<volatile int*>(last_flag) != 0;
-        ok = epi_sync();  // the flag is read before the next item can write it
-        if (!ok) break;
-        if (mine) {
+        if (*flag) {
           __threadfence();
-          for (int c = h; c < chunks; c += 2) {
-            float v[32];
+          // SR rows at a time, four parts' loads in flight together
+          constexpr int Q = SR / 4;
+#pragma unroll 1
+          for (int c = h; SR * c < it.nv; c += H) {
+            float v[SR];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            for (int i = 0; i < SR; ++i) v[i] = 0.f;
+#pragma unroll 1
+            for (int from = first; from <= last; from += 32) {
+              uint32_t left = with_part(from);
+#pragma unroll 1
+              while (left) {
+                float4 a[4][Q];
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              for (uint32_t left = has[k]; left;) {
-                // two parts' loads in flight together
-                const int s0 = first + 32 * k + __ffs(left) - 1;
-                left &= left - 1;
-                const int s1 = left ? first + 32 * k + __ffs(left) - 1 : -1;
-                left &= left - 1;
-                const float4* p0 = part_of(s0, s0 == first ? 1 : 0) + 8 * c * 128;
-                const float4* p1 = part_of(s1 < 0 ? s0 : s1, s1 < 0 && s0 == first ? 1 : 0) + 8 * c * 128;
-                float4 a[8], b[8];
+                for (int s = 0; s < 4; ++s) {
+                  const int piece = from + __ffs(left) - 1;
+                  const float4* src = part_of(max(piece, 0), piece == first ? 1 : 0) + Q * c * 128;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  a[i] = __ldcg(p0 + i * 128);
-                  b[i] = __ldcg(p1 + i * 128);
+                  for (int i = 0; i < Q; ++i) a[s][i] = left ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+                  left &= left - 1;
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  v[4 * i] += a[i].x;
-                  v[4 * i + 1] += a[i].y;
-                  v[4 * i + 2] += a[i].z;
-                  v[4 * i + 3] += a[i].w;
-                  if (s1 >= 0) {
-                    v[4 * i] += b[i].x;
-                    v[4 * i + 1] += b[i].y;
-                    v[4 * i + 2] += b[i].z;
-                    v[4 * i + 3] += b[i].w;
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                  for (int i = 0; i < Q; ++i) {
+                    v[4 * i] += a[s][i].x;
+                    v[4 * i + 1] += a[s][i].y;
+                    v[4 * i + 2] += a[s][i].z;
+                    v[4 * i + 3] += a[s][i].w;
                   }
-                }
               }
-            rows_out(c, v);
+            }
+            out_sr(c, v, 0);
           }
         }
       }
@@ -1080,23 +1216,24 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
 // One translation unit per kernel: gu_launch starts `pairs` clusters, gu_pairs
 // sets the kernel's attributes on the current device and returns how many
 // pairs fit at once (0: none).
-template <int OP, bool FP8, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int CHAIN>
 bool gu_launch(const GuParams& p, int pairs, cudaStream_t s);
-template <int OP, bool FP8, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int CHAIN>
 int gu_pairs();
 constexpr int kGuChain = 8;  // 16-bit products with fp32 outputs: 512 contracted values per chain
-#define MOE_GU_DECL(OP, FP8, CHAIN)                                                \
-  template <>                                                                      \
-  bool gu_launch<OP, FP8, CHAIN>(const GuParams& p, int pairs, cudaStream_t s);    \
-  template <>                                                                      \
-  int gu_pairs<OP, FP8, CHAIN>();
-MOE_GU_DECL(G_MM, false, 0)
-MOE_GU_DECL(G_MM, false, kGuChain)
-MOE_GU_DECL(G_DX, false, 0)
-MOE_GU_DECL(G_DX, false, kGuChain)
-MOE_GU_DECL(G_DW, false, 0)
-MOE_GU_DECL(G_DW, false, kGuChain)
-MOE_GU_DECL(G_MM, true, 1)
+#define MOE_GU_DECL(OP, FP8, ROWM, CHAIN)                                            \
+  template <>                                                                        \
+  bool gu_launch<OP, FP8, ROWM, CHAIN>(const GuParams& p, int pairs, cudaStream_t s); \
+  template <>                                                                        \
+  int gu_pairs<OP, FP8, ROWM, CHAIN>();
+MOE_GU_DECL(G_MM, false, false, 0)
+MOE_GU_DECL(G_MM, false, false, kGuChain)
+MOE_GU_DECL(G_DX, false, false, 0)
+MOE_GU_DECL(G_DX, false, false, kGuChain)
+MOE_GU_DECL(G_DW, false, true, 0)
+MOE_GU_DECL(G_DW, false, true, kGuChain)
+MOE_GU_DECL(G_MM, true, false, 1)
+MOE_GU_DECL(G_MM, true, true, 1)
 #undef MOE_GU_DECL
 
 }  // namespace moe

@@ -1,5 +1,6 @@
 // Grouped tensor-memory kernel: gradient of the weights.
 #define GU_OP G_DW
 #define GU_FP8 false
+#define GU_ROWM true
 #define GU_CHAIN 0
 #include "gu_inst.inl"

@@ -1,5 +1,6 @@
 // Grouped tensor-memory kernel: gradient of the weights, fp32 outputs.
 #define GU_OP G_DW
 #define GU_FP8 false
+#define GU_ROWM true
 #define GU_CHAIN kGuChain
 #include "gu_inst.inl"

@@ -1,5 +1,6 @@
 // Grouped tensor-memory kernel: gradient of the rows, fp32 outputs.
 #define GU_OP G_DX
 #define GU_FP8 false
+#define GU_ROWM false
 #define GU_CHAIN kGuChain
 #include "gu_inst.inl"

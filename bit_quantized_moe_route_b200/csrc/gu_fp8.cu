@@ -1,5 +1,6 @@
-// Grouped tensor-memory kernel: 8-bit forward.
+// Grouped tensor-memory kernel: 8-bit forward, few rows per expert.
 #define GU_OP G_MM
 #define GU_FP8 true
+#define GU_ROWM false
 #define GU_CHAIN 1
 #include "gu_inst.inl"

@@ -1,5 +1,6 @@
 // Grouped tensor-memory kernel: 16-bit forward.
 #define GU_OP G_MM
 #define GU_FP8 false
+#define GU_ROWM false
 #define GU_CHAIN 0
 #include "gu_inst.inl"

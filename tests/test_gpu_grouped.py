@@ -438,6 +438,14 @@ def test_fp8_row_counts(cuda_device, ws, counts):
     run_fp8(counts, 384, 256, FP, cuda_device, ws, pad=3)
 
 
+@pytest.mark.parametrize("out", [BF, FP])
+@pytest.mark.parametrize("n_in,n_out", [(256, 128), (128, 320), (144, 40), (640, 264), (1024, 1000), (384, 33)])
+def test_fp8_many_rows(cuda_device, ws, out, n_in, n_out):
+    """Many rows per expert on average, uneven, with short and empty experts among them."""
+    run_fp8([700, 0, 1, 513, 256, 255, 37, 900], n_in, n_out, out, cuda_device, ws, pad=9)
+    run_fp8([1500], n_in, n_out, out, cuda_device, ws, dense=True)
+
+
 @pytest.mark.parametrize("ld_pad,shift", [(16, 0), (48, 16), (3, 0), (0, 1), (16, 5)])
 def test_fp8_strides_and_alignment(cuda_device, ws, ld_pad, shift):
     run_fp8([5, 0, 70, 33], 256, 192, torch.float16 if shift == 5 else BF, cuda_device, ws, ld_pad=ld_pad, shift=shift)
