@@ -293,8 +293,10 @@ def alloc_grouped_workspace(device="cuda") -> torch.Tensor:
 
 def _rows_arg(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     """Leading dimension of a [rows, cols] matrix whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.is_contiguous():
+        return max(cols, 1)
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if rows > 1 and t.stride(0) < cols:
@@ -305,14 +307,15 @@ def _rows_arg(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
 def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
     if not first.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    dev = first.device
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"expected every tensor on {dev}, got one on {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"expected every tensor on {first.device}, got one on {t.device}")
 
 
 def _gmm_dims(dtype, out_dtype, offsets, experts: int, rows: int, n_out: int, n_in: int, ws) -> GmmDims:
-    if out_dtype not in _GMM_TYPES:
+    out = _GMM_TYPES.get(out_dtype)
+    if out is None:
         raise ValueError(f"output type {out_dtype} is not supported (bfloat16, float16, float32)")
     if dtype is not None and dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"operand type {dtype} is not supported (bfloat16, float16)")
@@ -320,17 +323,24 @@ def _gmm_dims(dtype, out_dtype, offsets, experts: int, rows: int, n_out: int, n_
         raise ValueError(f"expert_offsets must be int32 [{experts + 1}]")
     if ws.dtype != torch.uint8:
         raise ValueError("ws must be uint8 (alloc_grouped_workspace)")
-    return GmmDims(0 if dtype is None else _GMM_TYPES[dtype], _GMM_TYPES[out_dtype], experts, rows, n_out, n_in, 0)
+    return GmmDims(0 if dtype is None else _GMM_TYPES[dtype], out, experts, rows, n_out, n_in, 0)
 
 
-def _on_device(device, stream, call):
-    """Run call(stream handle) with the tensors' device current, on `stream` or that device's current stream."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream)
-    with torch.cuda.device(device):
-        return call(stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream)
+def _call(where: str, on: torch.Tensor, stream, *args):
+    """Call the entry point with the tensors' device current, on `stream` or that device's current stream."""
+    index = on.get_device()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device == on.device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {on.device}")
+    call = getattr(load_library(), where)
+    if index == torch.cuda.current_device():
+        _check(call(*args, handle), where)
+    else:
+        with torch.cuda.device(index):
+            _check(call(*args, handle), where)
 
 
 def grouped_mm(x, w, expert_offsets, y, ws, stream=None):
@@ -346,10 +356,8 @@ def grouped_mm(x, w, expert_offsets, y, ws, stream=None):
     ld_x, ld_y = _rows_arg(x, "x", R, n_in), _rows_arg(y, "y", R, n_out)
     d = _gmm_dims(x.dtype, y.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(x, w, expert_offsets, y, ws)
-    lib = load_library()
-    _check(_on_device(x.device, stream, lambda s: lib.moe_grouped_mm(
-        ctypes.byref(d), x.data_ptr(), ld_x, _ptr(w), _ptr(expert_offsets), y.data_ptr(), ld_y, _ptr(ws), ws.numel(),
-        s)), "moe_grouped_mm")
+    _call("moe_grouped_mm", x, stream, ctypes.byref(d), x.data_ptr(), ld_x, _ptr(w), _ptr(expert_offsets),
+          y.data_ptr(), ld_y, _ptr(ws), ws.numel())
 
 
 def grouped_mm_dx(dy, w, expert_offsets, dx, ws, stream=None):
@@ -361,10 +369,8 @@ def grouped_mm_dx(dy, w, expert_offsets, dx, ws, stream=None):
     ld_dy, ld_dx = _rows_arg(dy, "dy", R, n_out), _rows_arg(dx, "dx", R, n_in)
     d = _gmm_dims(dy.dtype, dx.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(dy, w, expert_offsets, dx, ws)
-    lib = load_library()
-    _check(_on_device(dy.device, stream, lambda s: lib.moe_grouped_mm_dx(
-        ctypes.byref(d), dy.data_ptr(), ld_dy, _ptr(w), _ptr(expert_offsets), dx.data_ptr(), ld_dx, _ptr(ws),
-        ws.numel(), s)), "moe_grouped_mm_dx")
+    _call("moe_grouped_mm_dx", dy, stream, ctypes.byref(d), dy.data_ptr(), ld_dy, _ptr(w), _ptr(expert_offsets),
+          dx.data_ptr(), ld_dx, _ptr(ws), ws.numel())
 
 
 def grouped_mm_dw(dy, x, expert_offsets, dw, ws, stream=None):
@@ -377,10 +383,8 @@ def grouped_mm_dw(dy, x, expert_offsets, dw, ws, stream=None):
     ld_dy, ld_x = _rows_arg(dy, "dy", R, n_out), _rows_arg(x, "x", R, n_in)
     d = _gmm_dims(x.dtype, dw.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(dy, x, expert_offsets, dw, ws)
-    lib = load_library()
-    _check(_on_device(dy.device, stream, lambda s: lib.moe_grouped_mm_dw(
-        ctypes.byref(d), dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, _ptr(expert_offsets), _ptr(dw), _ptr(ws),
-        ws.numel(), s)), "moe_grouped_mm_dw")
+    _call("moe_grouped_mm_dw", dy, stream, ctypes.byref(d), dy.data_ptr(), ld_dy, x.data_ptr(), ld_x,
+          _ptr(expert_offsets), _ptr(dw), _ptr(ws), ws.numel())
 
 
 def grouped_mm_fp8(x, x_scales, w, w_scales, expert_offsets, y, ws, stream=None):
@@ -403,10 +407,8 @@ def grouped_mm_fp8(x, x_scales, w, w_scales, expert_offsets, y, ws, stream=None)
     ld_x, ld_y = _rows_arg(x, "x", R, n_in), _rows_arg(y, "y", R, n_out)
     d = _gmm_dims(None, y.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(x, x_scales, w, w_scales, expert_offsets, y, ws)
-    lib = load_library()
-    _check(_on_device(x.device, stream, lambda s: lib.moe_grouped_mm_fp8(
-        ctypes.byref(d), x.data_ptr(), ld_x, _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(expert_offsets),
-        y.data_ptr(), ld_y, _ptr(ws), ws.numel(), s)), "moe_grouped_mm_fp8")
+    _call("moe_grouped_mm_fp8", x, stream, ctypes.byref(d), x.data_ptr(), ld_x, _ptr(x_scales), _ptr(w),
+          _ptr(w_scales), _ptr(expert_offsets), y.data_ptr(), ld_y, _ptr(ws), ws.numel())
 
 
 def quant_fp8(x, codes, scales, stream=None):
@@ -421,9 +423,7 @@ def quant_fp8(x, codes, scales, stream=None):
         raise ValueError(f"scales must be float32 [{(n_in + 127) // 128}, {R}]")
     ld = _rows_arg(x, "x", R, n_in)
     _one_device(x, codes, scales)
-    lib = load_library()
-    _check(_on_device(x.device, stream, lambda s: lib.moe_quant_fp8(
-        _GMM_TYPES[x.dtype], R, n_in, x.data_ptr(), ld, _ptr(codes), _ptr(scales), s)), "moe_quant_fp8")
+    _call("moe_quant_fp8", x, stream, _GMM_TYPES[x.dtype], R, n_in, x.data_ptr(), ld, _ptr(codes), _ptr(scales))
 
 
 FFN_AUTO, FFN_GEMV, FFN_TENSOR_CORE, FFN_DECODE_FUSED = 0, 1, 2, 3

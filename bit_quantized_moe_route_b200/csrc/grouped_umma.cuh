@@ -355,25 +355,24 @@ struct GuWalk {
     row = whole + lo;
   }
   MOE_DEV bool next(GuItem& it) {
-    if (row < whole) {
-      Tiles::get(p, l, row * cols + pair, it);
+    for (;;) {
+      const bool dealt = row < whole;
+      const int t = row - whole;
+      if (!dealt && (begin >= end || whole * cols + t >= n_tiles || l.tail[t] >= end)) return false;
+      Tiles::get(p, l, dealt ? row * cols + pair : whole * cols + t, it);
+      ++row;
       it.kb0 = 0;
       it.kb1 = it.nkb;
       it.pos = 0;
-      if (++row == whole) seek();
-      return true;
-    }
-    while (begin < end) {
-      const int t = row - whole;
-      if (whole * cols + t >= n_tiles || l.tail[t] >= end) break;
-      ++row;
-      Tiles::get(p, l, whole * cols + t, it);
+      if (dealt) {
+        if (row == whole) seek();
+        return true;
+      }
       it.pos = l.tail[t];
       it.kb0 = steps_before(begin, it);
       it.kb1 = steps_before(end, it);
       if (it.kb0 < it.kb1) return true;
     }
-    return false;
   }
   // steps of the tile that begin before `at`
   MOE_DEV static int steps_before(long long at, const GuItem& it) {
@@ -537,10 +536,12 @@ MOE_DEV uint4 gu_pack8(int type, const float* f) {
 // as 16-byte pieces where the rows allow it (`vec`: all 32 values there, 16-byte
 // aligned rows), else value by value.  `base`: element of the first row's first
 // value.
+template <int F32>
 MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int rows, int vals, bool vec, uint32_t buf) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
-  if (vec && type != G_FP32) {
+  const bool f32 = F32 < 0 ? type == G_FP32 : F32 == 1;
+  if (vec && !f32) {
     const int v = (lane & 3) * 8;
     float f[2][8];
 #pragma unroll
@@ -574,24 +575,58 @@ MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int 
   __syncwarp();
 }
 
+// 32 bytes to a 32-byte aligned address: one whole sector per lane and store
+// (with 16 the lanes of a warp, each in a row of its own, fill half sectors)
+MOE_DEV void gu_st256(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+MOE_DEV uint4 gu_bits4(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
 // Rows on the M side: W values of this lane's row, from element `base` on, of
-// which `left` are there; `vec`: 16-byte aligned rows.
-template <int W>
-MOE_DEV void gu_row_out(void* out, int type, long long base, int left, bool vec, const float* v) {
-  if (vec && left >= W) {
-    if (type == G_FP32) {
-      float* o = reinterpret_cast<float*>(out) + base;
+// which `left` are there; `unit`: the rows' alignment, 32, 16 or less.  F32:
+// what is known of the type (1: fp32, 0: 16 bits, -1: nothing).
+template <int W, int F32>
+MOE_DEV void gu_row_out(void* out, int type, long long base, int left, int unit, const float* v) {
+  const bool f32 = F32 < 0 ? type == G_FP32 : F32 == 1;
+  if (unit >= 16 && left >= W) {
+    char* o = reinterpret_cast<char*>(out) + base * (f32 ? 4 : 2);
+    if (f32) {
 #pragma unroll
-      for (int i = 0; i < W; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      for (int i = 0; i < W; i += 8) {
+        if (unit == 32) {
+          gu_st256(o + 4 * i, gu_bits4(v + i), gu_bits4(v + i + 4));
+        } else {
+          *reinterpret_cast<uint4*>(o + 4 * i) = gu_bits4(v + i);
+          *reinterpret_cast<uint4*>(o + 4 * i + 16) = gu_bits4(v + i + 4);
+        }
+      }
     } else {
-      uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
 #pragma unroll
-      for (int i = 0; i < W; i += 8) *reinterpret_cast<uint4*>(o + i) = gu_pack8(type, v + i);
+      for (int i = 0; i < W; i += 16) {
+        const uint4 a = gu_pack8(type, v + i), b = gu_pack8(type, v + i + 8);
+        if (unit == 32) {
+          gu_st256(o + 2 * i, a, b);
+        } else {
+          *reinterpret_cast<uint4*>(o + 2 * i) = a;
+          *reinterpret_cast<uint4*>(o + 2 * i + 16) = b;
+        }
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i)
-      if (i < left) gmm_store(out, type, base + i, v[i]);
+      if (i < left) {
+        if (f32) {
+          reinterpret_cast<float*>(out)[base + i] = v[i];
+        } else {
+          const uint16_t b = type == G_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[i]))
+                                            : __half_as_ushort(__float2half_rn(v[i]));
+          reinterpret_cast<uint16_t*>(out)[base + i] = b;
+        }
+      }
   }
 }
 
@@ -670,13 +705,15 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   }
   const int cols = (int)npairs;
   // The plan.  Only the item warp works from it (and the epilogue reads the
-  // cuts, after an item), so it makes it while the others set up, but for dw.
+  // cuts, after an item), so it makes it while the others set up; with many
+  // experts it takes the whole block (256 experts: 2.9 us, one warp 6.9).
   int whole = 0, n_tiles = -1;
-  if constexpr (OP == G_DW) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole);
+  const bool by_block = OP == G_DW || g.E > 64;
+  if (by_block) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole);
   tc_fence_before();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if constexpr (OP != G_DW)
-    if (warp == 3) n_tiles = gu_plan<OP, Tiles, 32>(g, line, lane, cols, p.split_most, &whole);
+    if (!by_block && warp == 3) n_tiles = gu_plan<OP, Tiles, 32>(g, line, lane, cols, p.split_most, &whole);
   if (warp == 3 && lane == 0 && n_tiles < 0) {
     set_error(g.err, kErrDeviceInput);
     line.cut[pair] = line.cut[pair + 1] = 0;
@@ -716,7 +753,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     if (warp == 0) {
       // ================= TMA issuer of this CTA's halves of both operands
       // (lane 0; all lanes share the many small copies of dw's last steps)
-      if (lane == 0) um_prefetch_map(&p.a_map);
+      if (lane == 0) {
+        um_prefetch_map(&p.a_map);
+        um_prefetch_map(&p.b_map[0]);
+      }
       GuItem it;
       int st = 0;
       uint32_t ph = 0;
@@ -938,7 +978,8 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * SR * 128);
     const long long ld = OP == G_DW ? g.n_in : g.ld_out;
     const int out_bytes = g.out_type == G_FP32 ? 4 : 2;
-    const bool rows_aligned = ld * out_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
+    const uintptr_t bits = (uintptr_t)(ld * out_bytes) | reinterpret_cast<uintptr_t>(g.out);
+    const int unit = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;  // the output rows' alignment
     GuRing ring;
     int seg = 0, slot = 0, joins = 0;
     uint32_t sph = 0, jph = 0;
@@ -964,7 +1005,6 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
       const int m = (int)rank * 128 + 32 * q;       // the warp's first M value in the tile
       const int vals = min(32, it.mv - m);          // how many it has
-      const bool vec = rows_aligned && (ROWM || vals == 32);
       // the first M and N value's output element (rows on the M side: this lane's row)
       const long long ob =
           ROWM ? (OP == G_DW ? (long long)it.e * g.n_out + it.m0 + m + lane : (long long)it.m0 + m + lane) * ld + it.n0
@@ -974,12 +1014,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         const int left = it.nv - SR * c;
         if (left <= 0 || vals <= 0) return;
         if constexpr (ROWM) {
-          if (lane < vals) gu_row_out<SR>(g.out, g.out_type, ob + SR * c, left, vec, &v[at]);
+          if (lane < vals) gu_row_out<SR, FP8 ? -1 : CHAIN ? 1 : 0>(g.out, g.out_type, ob + SR * c, left, unit, &v[at]);
         } else {
 #pragma unroll
           for (int i = 0; i < SR; ++i)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[at + i]) : "memory");
-          gu_rows_out(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, vec, buf);
+          gu_rows_out<FP8 ? -1 : CHAIN ? 1 : 0>(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
         }
       };
       auto put = [&](int c, const float (&v)[32]) {  // N values 32 c ..
