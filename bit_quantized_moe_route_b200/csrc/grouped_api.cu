@@ -107,14 +107,14 @@ moe_status_t launch_any(const GmmProblem& p, cudaStream_t s, int sms) {
 }
 
 // Resident pairs of a tensor-memory kernel on the current device (0: none).
-template <int OP, bool FP8, bool ROWM, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
 int resident_pairs() {
   static std::atomic<int> cached[64];  // pairs + 1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = cached[dev].load(std::memory_order_acquire);
   if (!v) {
-    v = gu_pairs<OP, FP8, ROWM, CHAIN>() + 1;
+    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN>() + 1;
     cached[dev].store(v, std::memory_order_release);
   }
   return v - 1;
@@ -136,9 +136,9 @@ bool umma_ok(const GmmProblem& p, int es) {
 // The 8-bit product has its rows on the M side from this mean per expert on.
 constexpr long long kRowsPerExpertM = 192;
 
-template <int OP, bool FP8, bool ROWM, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
-  const int pairs = resident_pairs<OP, FP8, ROWM, CHAIN>();
+  const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN>();
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
   const uint64_t es = FP8 ? 1 : 2;
   const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -171,9 +171,19 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
       GMM_TRY(api_tensor_map(ROWM ? &q.a_map : &q.b_map[i], dt, 2, p.rows_in, dims_r, st_r, box));
     }
   }
-  if (!gu_launch<OP, FP8, ROWM, CHAIN>(q, pairs, s))
+  if (!gu_launch<OP, FP8, ROWM, MT, CHAIN>(q, pairs, s))
     return api_fail(MOE_ERR_CUDA, "grouped_umma_kernel: %s", cudaGetErrorString(cudaGetLastError()));
   return MOE_OK;
+}
+
+// 512-value tiles where there are two or more for each pair of SMs (from the
+// host's side: as if every expert had rows).
+template <int OP>
+bool many_tiles(const GmmProblem& p) {
+  const long long m = ((OP == G_DX ? p.n_in : p.n_out) + 511) / 512;
+  const long long n = OP == G_DW ? (long long)p.E * ((p.n_in + kGuN - 1) / kGuN)
+                                 : std::max<long long>(p.rows / kGuN, std::min(p.E, p.rows));
+  return m * n >= 2 * kGuPairsMax;
 }
 
 template <int OP>
@@ -181,10 +191,11 @@ moe_status_t run_gmm(const GmmProblem& p, int in_type, void* ws, cudaStream_t s)
   if (umma_ok<OP>(p, in_type == G_E4M3 ? 1 : 2)) {
     if constexpr (OP == G_MM)
       if (in_type == G_E4M3)
-        return (long long)p.rows >= kRowsPerExpertM * p.E ? launch_umma<OP, true, true, 1>(p, in_type, ws, s)
-                                                          : launch_umma<OP, true, false, 1>(p, in_type, ws, s);
-    return p.out_type == G_FP32 ? launch_umma<OP, false, OP == G_DW, kGuChain>(p, in_type, ws, s)
-                                : launch_umma<OP, false, OP == G_DW, 0>(p, in_type, ws, s);
+        return (long long)p.rows >= kRowsPerExpertM * p.E ? launch_umma<OP, true, true, 1, 1>(p, in_type, ws, s)
+                                                          : launch_umma<OP, true, false, 1, 1>(p, in_type, ws, s);
+    if (p.out_type == G_FP32) return launch_umma<OP, false, OP == G_DW, 1, kGuChain>(p, in_type, ws, s);
+    return many_tiles<OP>(p) ? launch_umma<OP, false, OP == G_DW, 2, 0>(p, in_type, ws, s)
+                             : launch_umma<OP, false, OP == G_DW, 1, 0>(p, in_type, ws, s);
   }
   int sms = 0;
   if (sm_count(&sms)) return api_fail(MOE_ERR_CUDA, "device query failed");

@@ -19,7 +19,15 @@
 // from its registers and has one row scale; with them on the N side the M side
 // is the output's contiguous dimension.
 //
-// One tile step is 16 KB of A and up to 16 KB of B per CTA in a ring of six.
+// MT = 2 (16-bit products with enough tiles): a tile is 512 values of the M
+// side, two MMAs of 256 that share the B operand.  Per product that moves three
+// quarters of the bytes from L2 to the SMs, and those bytes are what a 1000 W
+// card runs out of first: 32,768 rows over 32 experts, in a loop, took 502 us
+// with 256 x 256 tiles at an SM clock of 1110 MHz, with the tensor pipe 81 %
+// busy at that clock.
+//
+// One tile step is MT x 16 KB of A and up to 16 KB of B per CTA, in a ring of
+// six (MT = 2: four).
 // M- and N-major operands are 64-value panels of 64 contracted rows.  For dw
 // the contracted rows are the expert's: in its last step only the rows that
 // are left are copied, in boxes of eight and one, and the rest of the last 16
@@ -65,8 +73,8 @@
 
 namespace moe {
 
-constexpr int kGuStages = 6;
-constexpr int kGuTile = 16384;            // bytes of one operand of one step
+constexpr int kGuTile = 16384;            // bytes of 128 operand rows of one step
+constexpr int kGuRing = 12 * kGuTile;
 constexpr int kGuN = 256;                 // output rows per tile
 // Warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 the epilogue, two for each 32
 // TMEM lanes.  (Sixteen epilogue warps were slower: each barrier wait and
@@ -78,7 +86,7 @@ constexpr int kGuStageRows = 16;          // output rows that a warp stores toge
 // CHAIN > 0: registers per thread at launch, and then of warps 0-3 and the epilogue
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
-constexpr int kGuScaleSlots = 6;
+constexpr int kGuScaleSlots = 5;
 constexpr int kGuScaleAhead = 4;          // slots whose copies are in flight
 constexpr int kGuItems = 4;               // items handed out ahead
 constexpr int kGuSegs = 8;                // sums between the MMA and the epilogue; TMEM slots
@@ -226,7 +234,7 @@ struct alignas(16) GuItem {
   int cost, r0, r1;        // of one step; dw: the expert's rows
   int kind;                // GuKind
   long long pos;           // where the tile begins on the line
-  int mv, pad;             // M values in use
+  int mv, halves;          // M values in use; MMAs of 256 of them (at most MT)
 };
 static_assert(sizeof(GuItem) == 64, "four 16-byte pieces");
 enum GuKind : int {
@@ -235,7 +243,7 @@ enum GuKind : int {
   GU_STOP = 2    // no more items
 };
 
-constexpr int kGuTailMost = 2 * kGuPairsMax;
+constexpr int kGuTailMost = 2 * 2 * kGuPairsMax;  // two tiles per pair, in halves
 
 // The plan of a launch (shared memory of each CTA; the same in all of them).
 struct alignas(16) GuLine {
@@ -250,15 +258,16 @@ struct alignas(16) GuLine {
 
 // shared memory from the first 1024-byte boundary: operand ring, scales, the
 // epilogue's rows on their way out, plan, barriers
-constexpr uint32_t kGuScaleOff = kGuStages * 2 * kGuTile;
+constexpr uint32_t kGuScaleOff = kGuRing;
 constexpr uint32_t kGuOutOff = kGuScaleOff + kGuScaleSlots * kGuN * 4;
 constexpr uint32_t kGuLineOff = kGuOutOff + kGuEpiWarps * kGuStageRows * 128;
 constexpr uint32_t kGuBarOff = kGuLineOff + sizeof(GuLine);
 constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
-template <int OP, bool FP8, bool ROWM>
+template <int OP, bool FP8, bool ROWM, int MT_>
 struct GuTiles {
+  static constexpr int MT = MT_;
   static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
   static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
   static constexpr int kRound = OP == G_DW ? 128 : 32;          // (dw: whole 64-value panels in both CTAs)
@@ -268,7 +277,7 @@ struct GuTiles {
   MOE_DEV static int n_all(const GmmProblem& p, int rows) {
     return OP == G_DW ? p.n_in : OP == G_MM && ROWM ? p.n_out : rows;
   }
-  MOE_DEV static int m_count(const GmmProblem& p, int rows) { return (m_all(p, rows) + 255) >> 8; }
+  MOE_DEV static int m_count(const GmmProblem& p, int rows) { return (m_all(p, rows) + 256 * MT - 1) / (256 * MT); }
   MOE_DEV static int n_count(int n) { return (n + kMost - 1) / kMost; }
   MOE_DEV static int of_expert(const GmmProblem& p, int rows) { return m_count(p, rows) * n_count(n_all(p, rows)); }
   MOE_DEV static int steps(const GmmProblem& p, int rows) {
@@ -282,7 +291,7 @@ struct GuTiles {
   MOE_DEV static int padded(int nv) { return max(kRound, (nv + kRound - 1) & ~(kRound - 1)); }
   // A step's cost is its operands' bytes (256 rows of A, np of B), between
   // that of reading weights from HBM (the same for every np) and that of the MMA.
-  MOE_DEV static int cost(int np) { return 256 + np; }
+  MOE_DEV static int cost(int np, int halves) { return 256 * halves + np; }
   // Tile g whole.  Neighbouring tiles share weights (mm, dx) or rows of x (dw).
   MOE_DEV static void get(const GmmProblem& p, const GuLine& l, int g, GuItem& it) {
     int lo = 0, hi = p.E;  // cum[lo] <= g < cum[hi]
@@ -298,8 +307,9 @@ struct GuTiles {
     const unsigned fast = (unsigned)(ROWM ? m_count(p, rows) : nt), tile = (unsigned)(g - l.cum[lo]);
     const int slow = (int)(tile / fast), quick = (int)(tile - (unsigned)slow * fast);
     const int t_m = ROWM ? quick : slow, t_n = ROWM ? slow : quick;
-    it.m0 = t_m * 256;
+    it.m0 = t_m * 256 * MT;
     it.mv = m_all(p, rows) - it.m0;
+    it.halves = MT == 1 || it.mv <= 256 ? 1 : 2;
     it.n0 = t_n * tn;
     it.nv = max(0, min(tn, n - it.n0));
     it.np = padded(it.nv);
@@ -309,7 +319,18 @@ struct GuTiles {
     }
     it.nkb = steps(p, rows);
     it.kind = OP == G_DW && rows == 0 ? GU_ZEROS : GU_RUN;
-    it.cost = cost(it.np);
+    it.cost = cost(it.np, it.halves);
+  }
+  // Of the tiles that are split, number t after the first `dealt`: halves of 256 M values.
+  MOE_DEV static void get_tail(const GmmProblem& p, const GuLine& l, int dealt, int t, GuItem& it) {
+    get(p, l, dealt + t / MT, it);
+    if (MT > 1) {
+      it.m0 += 256 * (t % MT);
+      it.mv -= 256 * (t % MT);
+      it.halves = 1;
+      it.cost = cost(it.np, 1);
+      if (it.mv <= 0) it.nkb = 0;  // (the tile has one half)
+    }
   }
 };
 
@@ -346,7 +367,7 @@ struct GuWalk {
   // to the piece's first tile: the last one that begins at or before it
   MOE_DEV void seek() {
     if (begin == end) return;
-    int lo = 0, hi = n_tiles - whole * cols;
+    int lo = 0, hi = (n_tiles - whole * cols) * Tiles::MT;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (l.tail[mid] <= begin) lo = mid;
@@ -358,8 +379,9 @@ struct GuWalk {
     for (;;) {
       const bool dealt = row < whole;
       const int t = row - whole;
-      if (!dealt && (begin >= end || whole * cols + t >= n_tiles || l.tail[t] >= end)) return false;
-      Tiles::get(p, l, dealt ? row * cols + pair : whole * cols + t, it);
+      if (!dealt && (begin >= end || t >= (n_tiles - whole * cols) * Tiles::MT || l.tail[t] >= end)) return false;
+      if (Tiles::MT == 1 || dealt) Tiles::get(p, l, dealt ? row * cols + pair : whole * cols + t, it);
+      else Tiles::get_tail(p, l, whole * cols, t, it);
       ++row;
       it.kb0 = 0;
       it.kb1 = it.nkb;
@@ -434,7 +456,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
     if (k > 0 && 32 * k + lane < p.E) l.cum[32 * k + lane] += before;
   }
   if (tid == 0) l.cum[p.E] = n_tiles;
-  const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = n_tiles - dealt;
+  const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = (n_tiles - dealt) * Tiles::MT;
   if constexpr (OP == G_DW)
     for (int i = tid; i < cols; i += NT) l.hand[i] = 0;
   sync();
@@ -449,14 +471,14 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
         const int n = (g1 + cols - 1 - q) / cols - (g0 + cols - 1 - q) / cols;  // tiles q, q + cols, ... among them
         c += (long long)n * Tiles::steps(p, l.off[e + 1] - l.off[e]);
       }
-      c *= Tiles::cost(Tiles::padded(Tiles::width(p.n_in, Tiles::n_count(p.n_in))));
+      c *= Tiles::cost(Tiles::padded(Tiles::width(p.n_in, Tiles::n_count(p.n_in))), Tiles::MT);
       atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[q]), (unsigned long long)c);
     }
   }
   // the costs of the tiles that are split (at most kGuTailMost - 1 of them)
   for (int i = tid; i < tails; i += NT) {
     GuItem it;
-    Tiles::get(p, l, dealt + i, it);
+    Tiles::get_tail(p, l, dealt, i, it);
     l.tail[i] = (long long)it.nkb * it.cost;
   }
   sync();
@@ -515,20 +537,18 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   return n_tiles;
 }
 
-// eight values as 16-bit pairs
-MOE_DEV uint4 gu_pack8(int type, const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (type == G_BF16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+// two values as a 16-bit pair, eight as four pairs
+MOE_DEV uint32_t gu_pack2(int type, float lo, float hi) {
+  if (type == G_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+MOE_DEV uint4 gu_pack8(int type, const float* f) {
+  return make_uint4(gu_pack2(type, f[0], f[1]), gu_pack2(type, f[2], f[3]), gu_pack2(type, f[4], f[5]),
+                    gu_pack2(type, f[6], f[7]));
 }
 
 // Rows on the N side leave through shared memory: a warp has 32 M values
@@ -630,14 +650,51 @@ MOE_DEV void gu_row_out(void* out, int type, long long base, int left, int unit,
   }
 }
 
+// The same two for 16 values that are rounded already: rows on the N side as
+// 16-bit words [row][lane] in `buf`; rows on the M side, pairs of this lane's row.
+MOE_DEV void gu_rows_out16(void* out, long long base, long long ld, int rows, int vals, bool vec, uint32_t buf) {
+  const int lane = threadIdx.x & 31;
+  uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
+  __syncwarp();
+  if (vec) {
+    const int r = lane >> 2, v = (lane & 3) * 8;
+    const uint4 a = tc_lds128(buf + 16u * lane), b = tc_lds128(buf + 512 + 16u * lane);
+    if (r < rows) *reinterpret_cast<uint4*>(o + r * ld + v) = a;
+    if (r + 8 < rows) *reinterpret_cast<uint4*>(o + (r + 8) * ld + v) = b;
+  } else if (lane < vals) {
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) o[r * ld + lane] = (uint16_t)um_lds16(buf + (uint32_t)(64 * r + 2 * lane));
+  }
+  __syncwarp();
+}
+MOE_DEV void gu_row_out16(void* out, long long base, int left, int unit, const uint32_t* w) {
+  uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
+  if (unit >= 16 && left >= 16) {
+    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
+    if (unit == 32) {
+      gu_st256(o, a, b);
+    } else {
+      *reinterpret_cast<uint4*>(o) = a;
+      *reinterpret_cast<uint4*>(o + 8) = b;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
 // ------------------------------------------------------------ the kernel
 // Launched in clusters of two CTAs (gridDim.x even), one CTA per SM.
-template <int OP, bool FP8, bool ROWM, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
 __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __grid_constant__ GuParams p) {
   constexpr int EW = kGuEpiWarps, H = EW / 4, SR = kGuStageRows;
   constexpr bool SCALE_RING = FP8 && !ROWM;  // the scales come through shared memory
   static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
-  using Tiles = GuTiles<OP, FP8, ROWM>;
+  static_assert(MT == 1 || CHAIN == 0, "register sums hold one MMA's");
+  constexpr int NS = 12 / (MT + 1);           // stages
+  constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
+  using Tiles = GuTiles<OP, FP8, ROWM, MT>;
   using Walk = GuWalk<Tiles>;
   constexpr bool A_MN = OP != G_MM, B_MN = OP == G_DW;
   constexpr int KE = Tiles::KE;
@@ -649,10 +706,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   GuLine& line = *reinterpret_cast<GuLine*>(gen + kGuLineOff);
   // (L): used in the leader CTA only
   auto full = [&](int s) { return bar + 8u * s; };                                      // (L) TMA bytes of both CTAs
-  auto empty = [&](int s) { return bar + 8u * (kGuStages + s); };                       // MMA commit
-  auto acc_full = [&](int b) { return bar + 8u * (2 * kGuStages + b); };                // MMA commit
-  auto acc_empty = [&](int b) { return bar + 8u * (2 * kGuStages + kGuSegs + b); };     // (L) epilogue warps, both CTAs
-  constexpr int kBarSc = 2 * kGuStages + 2 * kGuSegs;
+  auto empty = [&](int s) { return bar + 8u * (NS + s); };                       // MMA commit
+  auto acc_full = [&](int b) { return bar + 8u * (2 * NS + b); };                // MMA commit
+  auto acc_empty = [&](int b) { return bar + 8u * (2 * NS + kGuSegs + b); };     // (L) epilogue warps, both CTAs
+  constexpr int kBarSc = 2 * NS + 2 * kGuSegs;
   auto sc_full = [&](int s) { return bar + 8u * (kBarSc + s); };                        // scale warp
   auto sc_empty = [&](int s) { return bar + 8u * (kBarSc + kGuScaleSlots + s); };       // epilogue warps
   constexpr int kBarIt = kBarSc + 2 * kGuScaleSlots;
@@ -676,7 +733,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   const GmmProblem& g = p.g;
 
   if (tid == 0) {
-    for (int s = 0; s < kGuStages; ++s) {
+    for (int s = 0; s < NS; ++s) {
       tc_bar_init(full(s), 1);
       tc_bar_init(empty(s), 1);
     }
@@ -766,23 +823,24 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         const int half = it.np >> 1;
         const int m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
         const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-        const int panels = (half + 63) >> 6;  // dw
+        const int panels = (half + 63) >> 6, a_panels = 2 * it.halves;  // dw
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
           if (!ok) break;
-          const uint32_t a = base + (uint32_t)st * 2 * kGuTile, b = a + kGuTile;
+          const uint32_t a = base + (uint32_t)(st * kStep), b = a + MT * kGuTile;
           const uint32_t fb = cl_addr(full(st), 0);
           if constexpr (OP != G_DW) {
             if (lane == 0) {
-              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + (ROWM ? kGuTile : (16 << bx) * 128))));
+              if (leader) um_expect_tx(full(st), (uint32_t)(2 * (it.halves * kGuTile + (ROWM ? kGuTile : (16 << bx) * 128))));
               if constexpr (ROWM) {
                 gu_tma_2d(a, &p.a_map, kb * KE, m, fb);
                 gu_tma_3d(b, &p.b_map[0], kb * KE, n, it.e, fb);
               } else if constexpr (OP == G_MM) {
                 gu_tma_3d(a, &p.a_map, kb * KE, m, it.e, fb);
+                if (MT > 1 && it.halves > 1) gu_tma_3d(a + kGuTile, &p.a_map, kb * KE, m + 256, it.e, fb);
               } else {
-                gu_tma_3d(a, &p.a_map, m, kb * KE, it.e, fb);
-                gu_tma_3d(a + 8192, &p.a_map, m + 64, kb * KE, it.e, fb);
+                for (int q = 0; q < 2 * it.halves; ++q)
+                  gu_tma_3d(a + q * 8192, &p.a_map, m + 256 * (q >> 1) + 64 * (q & 1), kb * KE, it.e, fb);
               }
               if constexpr (!ROWM) gu_tma_2d(b, &p.b_map[bx], kb * KE, n, fb);
             }
@@ -790,9 +848,9 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
             const int y = it.r0 + kb * KE, left = it.r1 - y;
             if (left >= KE) {
               if (lane == 0) {
-                if (leader) um_expect_tx(full(st), (uint32_t)(2 * (kGuTile + panels * 8192)));
-                gu_tma_2d(a, &p.a_map, m, y, fb);
-                gu_tma_2d(a + 8192, &p.a_map, m + 64, y, fb);
+                if (leader) um_expect_tx(full(st), (uint32_t)(2 * (a_panels + panels) * 8192));
+                for (int q = 0; q < a_panels; ++q)
+                  gu_tma_2d(a + q * 8192, &p.a_map, m + 256 * (q >> 1) + 64 * (q & 1), y, fb);
                 for (int q = 0; q < panels; ++q) gu_tma_2d(b + q * 8192, &p.b_map[0], n + 64 * q, y, fb);
               }
             } else {
@@ -802,20 +860,22 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
               // zero rows if the multiple of 16 is not reached.
               const int fill = (left + 15) & ~15, eights = left >> 3, ones = left & 7 ? 8 : 0;
               const int zeros = fill - 8 * eights - ones > 0 ? 1 : 0, pieces = eights + ones + zeros;
-              if (lane == 0 && leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (2 + panels)));
+              if (lane == 0 && leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (a_panels + panels)));
               __syncwarp();
-              for (int i = lane; i < pieces * (2 + panels); i += 32) {
+              for (int i = lane; i < pieces * (a_panels + panels); i += 32) {
                 const int q = i / pieces, w = i - q * pieces;
                 const bool one = w >= eights && w < eights + ones;
                 const int r = w < eights ? 8 * w : one ? 8 * eights + w - eights : 8 * eights + ones;
-                const uint32_t dst = (q < 2 ? a + q * 8192 : b + (q - 2) * 8192) + (uint32_t)(r * 128);
-                const CUtensorMap* maps = q < 2 ? p.a_tail : p.b_tail;
-                gu_tma_2d(dst, &maps[one ? 1 : 0], q < 2 ? m + 64 * q : n + 64 * (q - 2), r < left ? y + r : g.rows, fb);
+                const bool is_a = q < a_panels;
+                const uint32_t dst = (is_a ? a + q * 8192 : b + (q - a_panels) * 8192) + (uint32_t)(r * 128);
+                const CUtensorMap* maps = is_a ? p.a_tail : p.b_tail;
+                const int x = is_a ? m + 256 * (q >> 1) + 64 * (q & 1) : n + 64 * (q - a_panels);
+                gu_tma_2d(dst, &maps[one ? 1 : 0], x, r < left ? y + r : g.rows, fb);
               }
               __syncwarp();
             }
           }
-          if (++st == kGuStages) st = 0, ph ^= 1u;
+          if (++st == NS) st = 0, ph ^= 1u;
         }
       }
       if (!ok) {  // a wait gave up: let the copies in flight land before this CTA's memory is released
@@ -827,7 +887,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     } else if (warp == 1) {
       // ================= MMA issuer (leader CTA)
       if (leader && lane == 0) {
-        GuItem it;
+        GuItem it = {};
         int st = 0, seg = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -838,62 +898,104 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         for (int i = 0; i < kGuSegs; ++i) user[i] = -1;
         const uint32_t idesc0 = (1u << 4) | ((uint32_t)(p.type == G_BF16 ? 1 : 0) * ((1u << 7) | (1u << 10))) |
                                 ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | (16u << 24);
-        const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + kGuTile, B_MN);
+        const uint64_t da0 = gu_desc(base, A_MN), db0 = gu_desc(base + MT * kGuTile, B_MN);
+        // TMEM slots for the next sum, n wide: its first column.  The sums
+        // leave the epilogue in order, so all that used these slots or this
+        // barrier (eight sums ago) are through once the latest of them is.
+        // One already seen through is not waited for again: its barrier may be
+        // phases ahead.
+        auto open_sum = [&](int n, uint32_t& d) {
+          const int at = ring.take(n);
+          int before = seg - kGuSegs;
+#pragma unroll
+          for (int i = 0; i < kGuSegs; ++i)
+            if (i >= at && i < at + ring.used) {
+              before = max(before, user[i]);
+              user[i] = seg;
+            }
+          ++seg;
+          d = tmem + (uint32_t)at * kGuSlotCols;
+          if (before > done) {
+            if (!cl_bar_wait(acc_empty(before & (kGuSegs - 1)), (uint32_t)(before / kGuSegs) & 1u, abort_flag)) return false;
+            done = before;
+          }
+          tc_fence_after();
+          return true;
+        };
+        // the MMAs of one step's stage s for the h-th 256 M values
+        auto step_mma = [&](int s, int h, int kb, uint32_t d, uint32_t idesc, uint32_t acc) {
+          const uint64_t so = (uint64_t)((uint32_t)(s * kStep) >> 4), ao = so + (uint64_t)((uint32_t)(h * kGuTile) >> 4);
+          int steps = 4;
+          if constexpr (OP == G_DW) steps = min(4, (it.r1 - it.r0 - kb * KE + 15) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (OP != G_DW || k < steps) {
+              // 16 (e4m3: 32) contracted values: 32 bytes along a K-major row, 16 rows of a panel otherwise
+              gu_mma<FP8>(d, da0 + ao + (uint64_t)((A_MN ? 2048 : 32) * k >> 4),
+                          db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
+              acc = 1;
+            }
+        };
         while (ok && copy_item(it, true)) {
           if (it.kind == GU_ZEROS) continue;
           const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
+          if (MT > 1 && it.halves > 1) {
+            // Both halves of the tile.  The second half's accumulator is still
+            // being read when the first half's is free: the first steps, as
+            // many as there are stages, are done for the first half, then for
+            // the second.
+            uint32_t d0, d1;
+            ok = open_sum(it.np, d0);
+            const int lead = min(NS, it.nkb);
+            int s1 = st;
+            for (int kb = 0; ok && kb < lead; ++kb) {
+              ok = cl_bar_wait(full(s1), s1 < st ? ph ^ 1u : ph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              step_mma(s1, 0, kb, d0, idesc, kb > 0);
+              if (++s1 == NS) s1 = 0;
+            }
+            if (!ok) break;
+            const int seg0 = (seg - 1) & (kGuSegs - 1);
+            if (lead == it.nkb) umma2_commit_both(acc_full(seg0));
+            ok = open_sum(it.np, d1);
+            if (!ok) break;
+            for (int kb = 0; kb < it.nkb; ++kb) {
+              if (kb >= lead) {
+                ok = cl_bar_wait(full(st), ph, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                step_mma(st, 0, kb, d0, idesc, 1u);
+                if (kb + 1 == it.nkb) umma2_commit_both(acc_full(seg0));
+              }
+              step_mma(st, 1, kb, d1, idesc, kb > 0);
+              umma2_commit_both(empty(st));
+              if (++st == NS) st = 0, ph ^= 1u;
+            }
+            if (!ok) break;
+            umma2_commit_both(acc_full((seg - 1) & (kGuSegs - 1)));
+            continue;
+          }
           for (int kb = it.kb0; kb < it.kb1;) {
             const int stride = SCALE_RING ? gu_stride(it.np) : kGuN;
             const int kend = SCALE_RING ? min(it.kb1, kb + kGuN / stride) : CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
-            // The sums leave the epilogue in order, so all that used these
-            // slots or this barrier (eight sums ago) are through once the
-            // latest of them is.  One already seen through is not waited for
-            // again: its barrier may be phases ahead.
-            const int at = ring.take(FP8 ? kGuN : it.np);
-            int before = seg - kGuSegs;
-#pragma unroll
-            for (int i = 0; i < kGuSegs; ++i)
-              if (i >= at && i < at + ring.used) {
-                before = max(before, user[i]);
-                user[i] = seg;
-              }
-            if (before > done) {
-              if (!cl_bar_wait(acc_empty(before & (kGuSegs - 1)), (uint32_t)(before / kGuSegs) & 1u, abort_flag)) {
-                ok = false;
-                break;
-              }
-              done = before;
-            }
-            tc_fence_after();
-            uint32_t d = tmem + (uint32_t)at * kGuSlotCols;
-            uint32_t acc = 0;
-            for (; kb < kend; ++kb) {
-              if (!cl_bar_wait(full(st), ph, abort_flag)) {
-                ok = false;
-                break;
-              }
+            uint32_t d, acc = 0;
+            ok = open_sum(FP8 ? kGuN : it.np, d);
+            for (; ok && kb < kend; ++kb) {
+              ok = cl_bar_wait(full(st), ph, abort_flag);
+              if (!ok) break;
               tc_fence_after();
-              const uint64_t so = (uint64_t)((uint32_t)st * 2 * kGuTile >> 4);
-              int steps = 4;
-              if constexpr (OP == G_DW) steps = min(4, (it.r1 - it.r0 - kb * KE + 15) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (OP != G_DW || k < steps) {
-                  // 16 (e4m3: 32) contracted values: 32 bytes along a K-major row, 16 rows of a panel otherwise
-                  gu_mma<FP8>(d, da0 + so + (uint64_t)((A_MN ? 2048 : 32) * k >> 4),
-                              db0 + so + (uint64_t)((B_MN ? 2048 : 32) * k >> 4), idesc, acc);
-                  acc = 1;
-                }
+              step_mma(st, 0, kb, d, idesc, acc);
+              acc = 1;
               if constexpr (SCALE_RING) {
                 acc = 0;
                 d += stride;
               }
               umma2_commit_both(empty(st));
-              if (++st == kGuStages) st = 0, ph ^= 1u;
+              if (++st == NS) st = 0, ph ^= 1u;
             }
             if (!ok) break;
-            umma2_commit_both(acc_full(seg & (kGuSegs - 1)));
-            ++seg;
+            umma2_commit_both(acc_full((seg - 1) & (kGuSegs - 1)));
           }
         }
         umma2_commit_both(drain);
@@ -1004,9 +1106,9 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       const int chunks = (it.np + 31) >> 5;
       const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
       const int m = (int)rank * 128 + 32 * q;       // the warp's first M value in the tile
-      const int vals = min(32, it.mv - m);          // how many it has
+      int vals = min(32, it.mv - m);                // how many it has
       // the first M and N value's output element (rows on the M side: this lane's row)
-      const long long ob =
+      long long ob =
           ROWM ? (OP == G_DW ? (long long)it.e * g.n_out + it.m0 + m + lane : (long long)it.m0 + m + lane) * ld + it.n0
                : (long long)it.n0 * ld + it.m0 + m;
       // N values SR c .. of the tile, from v[at] on
@@ -1037,7 +1139,11 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         float z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0.f;
-        for (int c = h; c < chunks; c += H) put(c, z);
+        for (int half = 0; half < it.halves; ++half) {
+          for (int c = h; c < chunks; c += H) put(c, z);
+          ob += ROWM ? 256 * ld : 256;
+          vals = min(32, it.mv - 256 - m);
+        }
         continue;
       }
       auto wait_sums = [&]() {
@@ -1052,16 +1158,59 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         if (lane == 0) cl_arrive(cl_addr(acc_empty(seg & (kGuSegs - 1)), 0));
       };
       if constexpr (CHAIN == 0) {
-        const int at = ring.take(it.np);
-        ok = wait_sums();
-        if (!ok) break;
-        for (int c = h; c < chunks; c += H) {
-          float v[32];
-          gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
-          put(c, v);
+        for (int half = 0; half < it.halves; ++half) {
+          const int at = ring.take(it.np);
+          ok = wait_sums();
+          if (!ok) break;
+          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+          if (all) {
+            // rounded to the output's 16 bits on the way into registers, so
+            // that the accumulator is free before the first store
+            uint32_t w[4][16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (H * j + h < chunks) {
+                float v[32];
+                gu_ld32(ta + 64u * j, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[j][i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+              }
+            give_back();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (H * j + h < chunks) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const int c = 2 * (H * j + h) + u, left = it.nv - SR * c;
+                  if (left <= 0 || vals <= 0) continue;
+                  if constexpr (ROWM) {
+                    if (lane < vals) gu_row_out16(g.out, ob + SR * c, left, unit, &w[j][8 * u]);
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const uint32_t to = buf + (uint32_t)(128 * i + 2 * lane), x = w[j][8 * u + i];
+                      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"((uint16_t)x) : "memory");
+                      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64), "h"((uint16_t)(x >> 16)) : "memory");
+                    }
+                    gu_rows_out16(g.out, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
+                  }
+                }
+              }
+          } else {
+            for (int c = h; c < chunks; c += H) {
+              float v[32];
+              gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
+              put(c, v);
+            }
+            give_back();
+          }
+          ++seg;
+          if (half + 1 < it.halves) {  // the second half's M values
+            ob += ROWM ? 256 * ld : 256;
+            vals = min(32, it.mv - 256 - m);
+          }
         }
-        give_back();
-        ++seg;
+        if (!ok) break;
       } else {
         // sums in pairs of columns, for the packed fp32 instructions
         constexpr int NJ = Tiles::kMost / 64;
@@ -1256,24 +1405,27 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
 // One translation unit per kernel: gu_launch starts `pairs` clusters, gu_pairs
 // sets the kernel's attributes on the current device and returns how many
 // pairs fit at once (0: none).
-template <int OP, bool FP8, bool ROWM, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
 bool gu_launch(const GuParams& p, int pairs, cudaStream_t s);
-template <int OP, bool FP8, bool ROWM, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
 int gu_pairs();
 constexpr int kGuChain = 8;  // 16-bit products with fp32 outputs: 512 contracted values per chain
-#define MOE_GU_DECL(OP, FP8, ROWM, CHAIN)                                            \
-  template <>                                                                        \
-  bool gu_launch<OP, FP8, ROWM, CHAIN>(const GuParams& p, int pairs, cudaStream_t s); \
-  template <>                                                                        \
-  int gu_pairs<OP, FP8, ROWM, CHAIN>();
-MOE_GU_DECL(G_MM, false, false, 0)
-MOE_GU_DECL(G_MM, false, false, kGuChain)
-MOE_GU_DECL(G_DX, false, false, 0)
-MOE_GU_DECL(G_DX, false, false, kGuChain)
-MOE_GU_DECL(G_DW, false, true, 0)
-MOE_GU_DECL(G_DW, false, true, kGuChain)
-MOE_GU_DECL(G_MM, true, false, 1)
-MOE_GU_DECL(G_MM, true, true, 1)
+#define MOE_GU_DECL(OP, FP8, ROWM, MT, CHAIN)                                             \
+  template <>                                                                             \
+  bool gu_launch<OP, FP8, ROWM, MT, CHAIN>(const GuParams& p, int pairs, cudaStream_t s); \
+  template <>                                                                             \
+  int gu_pairs<OP, FP8, ROWM, MT, CHAIN>();
+MOE_GU_DECL(G_MM, false, false, 1, 0)
+MOE_GU_DECL(G_MM, false, false, 2, 0)
+MOE_GU_DECL(G_MM, false, false, 1, kGuChain)
+MOE_GU_DECL(G_DX, false, false, 1, 0)
+MOE_GU_DECL(G_DX, false, false, 2, 0)
+MOE_GU_DECL(G_DX, false, false, 1, kGuChain)
+MOE_GU_DECL(G_DW, false, true, 1, 0)
+MOE_GU_DECL(G_DW, false, true, 2, 0)
+MOE_GU_DECL(G_DW, false, true, 1, kGuChain)
+MOE_GU_DECL(G_MM, true, false, 1, 1)
+MOE_GU_DECL(G_MM, true, true, 1, 1)
 #undef MOE_GU_DECL
 
 }  // namespace moe

@@ -2,5 +2,6 @@
 #define GU_OP G_DW
 #define GU_FP8 false
 #define GU_ROWM true
+#define GU_MT 1
 #define GU_CHAIN kGuChain
 #include "gu_inst.inl"

@@ -1,0 +1,7 @@
+// Grouped tensor-memory kernel: gradient of the weights, 512-value tiles.
+#define GU_OP G_DW
+#define GU_FP8 false
+#define GU_ROWM true
+#define GU_MT 2
+#define GU_CHAIN 0
+#include "gu_inst.inl"

@@ -2,5 +2,6 @@
 #define GU_OP G_DX
 #define GU_FP8 false
 #define GU_ROWM false
+#define GU_MT 1
 #define GU_CHAIN kGuChain
 #include "gu_inst.inl"

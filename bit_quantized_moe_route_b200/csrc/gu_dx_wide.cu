@@ -1,0 +1,7 @@
+// Grouped tensor-memory kernel: gradient of the rows, 512-value tiles.
+#define GU_OP G_DX
+#define GU_FP8 false
+#define GU_ROWM false
+#define GU_MT 2
+#define GU_CHAIN 0
+#include "gu_inst.inl"

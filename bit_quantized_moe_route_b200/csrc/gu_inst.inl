@@ -1,5 +1,5 @@
 // Instantiation unit of the grouped tensor-memory kernel (GU_OP, GU_FP8,
-// GU_ROWM, GU_CHAIN set by the including file).
+// GU_ROWM, GU_MT, GU_CHAIN set by the including file).
 #include "grouped_umma.cuh"
 
 namespace moe {
@@ -22,22 +22,22 @@ cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* att
 }  // namespace
 
 template <>
-bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>(const GuParams& p, int pairs, cudaStream_t s) {
+bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>(const GuParams& p, int pairs, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
-  return cudaLaunchKernelEx(&cfg, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>, p) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, p) == cudaSuccess;
 }
 
 template <>
-int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>() {
-  if (cudaFuncSetAttribute(grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>() {
+  if (cudaFuncSetAttribute(grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)gu_smem()) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   // the register hand-over of these kernels counts on what the block starts with
   cudaFuncAttributes fa;
-  if (GU_CHAIN > 0 && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>) != cudaSuccess ||
+  if (GU_CHAIN > 0 && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>) != cudaSuccess ||
                        fa.numRegs != kGuRegs)) {
     cudaGetLastError();
     return 0;
@@ -45,7 +45,7 @@ int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>() {
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_CHAIN>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }

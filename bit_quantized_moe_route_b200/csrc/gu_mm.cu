@@ -2,5 +2,6 @@
 #define GU_OP G_MM
 #define GU_FP8 false
 #define GU_ROWM false
+#define GU_MT 1
 #define GU_CHAIN 0
 #include "gu_inst.inl"

@@ -169,6 +169,17 @@ def test_many_experts(cuda_device, ws, op):
     run_op(op, counts, 64, 72, BF, BF, cuda_device, ws)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("op,counts,wide,other", [
+    ("mm", [300, 0, 1, 77, 256, 513, 40, 33] * 5, 2348, 1024), ("mm", [90] * 40, 2304, 200), ("mm", [3] * 80, 1100, 64),
+    ("dx", [300, 0, 1, 77, 256, 513, 40, 33] * 5, 2344, 1024), ("dx", [90] * 40, 2304, 200), ("dx", [3] * 80, 1096, 64),
+    ("dw", [300, 0, 1, 77, 256, 513, 40, 1300] * 5, 1000, 520), ("dw", [65] * 40, 776, 328), ("dw", [0] * 100, 512, 512)])
+def test_many_tiles(cuda_device, ws, dtype, op, counts, wide, other):
+    """Enough tiles for the widest ones: their odd last halves, short and long sums, whole and split tiles."""
+    n_in, n_out = {"mm": (other, wide), "dx": (wide, other), "dw": (other, wide)}[op]
+    run_op(op, counts, n_in, n_out, dtype, dtype, cuda_device, ws, pad=5, start=3 if op != "dw" else 0)
+
+
 @pytest.mark.parametrize("op", ["mm", "dx", "fp8"])
 @pytest.mark.parametrize("seed", range(3))
 def test_mixed_tile_widths(cuda_device, ws, op, seed):
