@@ -83,7 +83,9 @@ constexpr int kGuN = 256;                 // output rows per tile
 constexpr int kGuEpiWarps = 8;
 constexpr int kGuThreads = 128 + 32 * kGuEpiWarps;
 constexpr int kGuStageRows = 16;          // output rows that a warp stores together
-// CHAIN > 0: registers per thread at launch, and then of warps 0-3 and the epilogue
+// Registers per thread at launch and, where the epilogue holds a tile's sums or
+// rounded outputs, then of warps 0-3 and of the epilogue.
+constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
 constexpr int kGuScaleSlots = 5;
@@ -805,8 +807,8 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   };
 
   if (warp < 4) {
-    // the sums of CHAIN > 0 are the epilogue's registers (the host checks that the block has kGuRegs per thread)
-    if constexpr (CHAIN > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
+    // the epilogue gets registers of these warps (the host checks that the block has kGuRegs per thread)
+    if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
     if (warp == 0) {
       // ================= TMA issuer of this CTA's halves of both operands
       // (lane 0; all lanes share the many small copies of dw's last steps)
@@ -1074,7 +1076,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       __syncwarp();
     }
   } else {
-    if constexpr (CHAIN > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
+    if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every H-th 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * SR * 128);
@@ -1158,24 +1160,35 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         if (lane == 0) cl_arrive(cl_addr(acc_empty(seg & (kGuSegs - 1)), 0));
       };
       if constexpr (CHAIN == 0) {
-        for (int half = 0; half < it.halves; ++half) {
-          const int at = ring.take(it.np);
-          ok = wait_sums();
-          if (!ok) break;
-          const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
-          if (all) {
-            // rounded to the output's 16 bits on the way into registers, so
-            // that the accumulator is free before the first store
-            uint32_t w[4][16];
+        if (all) {
+          // Rounded to the output's 16 bits on the way into registers, both
+          // halves, so that the accumulators are free before the first store:
+          // the next tile's MMAs wait for 800 clocks of TMEM reads then, and
+          // not for 4,800 more of stores.
+          uint32_t w[MT][4][16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (H * j + h < chunks) {
-                float v[32];
-                gu_ld32(ta + 64u * j, v);
+          for (int half = 0; half < MT; ++half)
+            if (half < it.halves) {
+              const int at = ring.take(it.np);
+              ok = ok && wait_sums();
+              if (ok) {
+                const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[j][i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+                for (int j = 0; j < 4; ++j)
+                  if (H * j + h < chunks) {
+                    float v[32];
+                    gu_ld32(ta + 64u * j, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[half][j][i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+                  }
+                give_back();
+                ++seg;
               }
-            give_back();
+            }
+          if (!ok) break;
+#pragma unroll
+          for (int half = 0; half < MT; ++half) {
+            if (half >= it.halves) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (H * j + h < chunks) {
@@ -1184,11 +1197,11 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                   const int c = 2 * (H * j + h) + u, left = it.nv - SR * c;
                   if (left <= 0 || vals <= 0) continue;
                   if constexpr (ROWM) {
-                    if (lane < vals) gu_row_out16(g.out, ob + SR * c, left, unit, &w[j][8 * u]);
+                    if (lane < vals) gu_row_out16(g.out, ob + SR * c, left, unit, &w[half][j][8 * u]);
                   } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                      const uint32_t to = buf + (uint32_t)(128 * i + 2 * lane), x = w[j][8 * u + i];
+                      const uint32_t to = buf + (uint32_t)(128 * i + 2 * lane), x = w[half][j][8 * u + i];
                       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"((uint16_t)x) : "memory");
                       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64), "h"((uint16_t)(x >> 16)) : "memory");
                     }
@@ -1196,21 +1209,21 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                   }
                 }
               }
-          } else {
-            for (int c = h; c < chunks; c += H) {
-              float v[32];
-              gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
-              put(c, v);
-            }
-            give_back();
-          }
-          ++seg;
-          if (half + 1 < it.halves) {  // the second half's M values
-            ob += ROWM ? 256 * ld : 256;
+            ob += ROWM ? 256 * ld : 256;  // the second half's M values
             vals = min(32, it.mv - 256 - m);
           }
+        } else {
+          const int at = ring.take(it.np);
+          ok = wait_sums();
+          if (!ok) break;
+          for (int c = h; c < chunks; c += H) {
+            float v[32];
+            gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
+            put(c, v);
+          }
+          give_back();
+          ++seg;
         }
-        if (!ok) break;
       } else {
         // sums in pairs of columns, for the packed fp32 instructions
         constexpr int NJ = Tiles::kMost / 64;

@@ -37,8 +37,8 @@ int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>() {
   }
   // the register hand-over of these kernels counts on what the block starts with
   cudaFuncAttributes fa;
-  if (GU_CHAIN > 0 && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>) != cudaSuccess ||
-                       fa.numRegs != kGuRegs)) {
+  if (gu_hand_over(GU_MT, GU_CHAIN) && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>) != cudaSuccess ||
+                       (fa.numRegs + 7) / 8 * 8 != kGuRegs)) {
     cudaGetLastError();
     return 0;
   }
