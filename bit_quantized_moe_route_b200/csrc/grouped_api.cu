@@ -152,9 +152,8 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
   if constexpr (OP == G_DW) {
     const uint64_t dims_x[2] = {(uint64_t)p.n_in, (uint64_t)p.rows}, st_x[1] = {(uint64_t)p.ld_x * es};
     const uint64_t dims_y[2] = {(uint64_t)p.n_out, (uint64_t)p.rows}, st_y[1] = {(uint64_t)p.ld_rows * es};
-    const uint32_t rows[3] = {64, 8, 1};
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t box[2] = {inner, rows[i]};
+    for (int i = 0; i < 7; ++i) {
+      const uint32_t box[2] = {inner, 64u >> i};
       GMM_TRY(api_tensor_map(i ? &q.a_tail[i - 1] : &q.a_map, dt, 2, p.rows_in, dims_y, st_y, box));
       GMM_TRY(api_tensor_map(i ? &q.b_tail[i - 1] : &q.b_map[0], dt, 2, p.x, dims_x, st_x, box));
     }

@@ -3,7 +3,7 @@
 //
 // A tile is 256 values of the M side (128 per CTA of the pair) by up to 256 of
 // the N side: where that is the rows of an expert, they are cut into equal
-// tiles of at most 256 (8-bit: 128), rounded up to 32, so that an expert with
+// tiles of at most 256 (8-bit: 128), rounded up to 16 (32), so that an expert with
 // few rows costs a narrow MMA and not a padded tile.  Steps of the
 // contracted dimension are 128 bytes per row: 64 16-bit values or 128 e4m3
 // codes, the block of the 8-bit scales.
@@ -30,7 +30,7 @@
 // six (MT = 2: four).
 // M- and N-major operands are 64-value panels of 64 contracted rows.  For dw
 // the contracted rows are the expert's: in its last step only the rows that
-// are left are copied, in boxes of eight and one, and the rest of the last 16
+// are left are copied, in boxes of 32 rows to one, and the rest of the last 16
 // comes from beyond the tensor's end, which TMA fills with zeros, so that no
 // value of another expert's rows (a NaN, say) enters a product.
 //
@@ -39,9 +39,11 @@
 // weights and rows from L2 (with each pair on a run of neighbouring tiles
 // instead, 74 pairs stream 148 MB between two uses of an operand tile, more
 // than L2 holds: 32,768 rows over 32 experts took 870 us that way, 588 dealt
-// out).  All but the last one to two tiles per pair are dealt whole.  Those
-// last ones are split by steps: their steps are one line, cut so that every
-// pair has the same cost in all.  A tile that a cut goes through is summed by
+// out).  All but the last one to two tiles per pair are dealt whole, and as
+// many of the rest's halves as there are for all pairs.  What is then left is
+// cut evenly, a number of pairs to each, or (dw, whose tiles differ in length,
+// and few tiles) by steps: their steps are one line, cut so that every pair
+// has the same cost in all.  A tile that a cut goes through is summed by
 // the pairs that hold parts of it: each writes its fp32 partial sums to the
 // workspace and counts itself in; the last one adds the partials in the
 // pieces' order (so the result does not depend on who was last) and writes
@@ -104,9 +106,9 @@ static_assert(kGuCounters + kGuPairsMax * 2 * 4 <= kGuParts, "counters");
 static_assert(kGuParts + (size_t)kGuPairsMax * 4 * kGuPart <= kGuWsBytes, "workspace");
 
 struct alignas(64) GuParams {
-  CUtensorMap a_map;     // mm, dx: W; dw: x, 64 rows
-  CUtensorMap b_map[4];  // mm, dx: rows in boxes of 16, 32, 64, 128; dw: dy, 64 rows
-  CUtensorMap a_tail[2], b_tail[2];  // dw: boxes of eight rows and of one
+  CUtensorMap a_map;     // mm, dx: W; dw: dy, 64 rows
+  CUtensorMap b_map[4];  // mm, dx: rows in boxes of 16, 32, 64, 128; dw: x, 64 rows
+  CUtensorMap a_tail[6], b_tail[6];  // dw: boxes of 32, 16, .. 1 rows
   GmmProblem g;
   int type;              // GmmType of the operands
   int split_most;        // pieces that a tile may be cut into
@@ -272,7 +274,8 @@ struct GuTiles {
   static constexpr int MT = MT_;
   static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
   static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
-  static constexpr int kRound = OP == G_DW ? 128 : 32;          // (dw: whole 64-value panels in both CTAs)
+  // N values per MMA in multiples of 16 (8-bit: 32; dw: whole 64-value panels in both CTAs)
+  static constexpr int kRound = OP == G_DW ? 128 : FP8 ? 32 : 16;
   MOE_DEV static int m_all(const GmmProblem& p, int rows) {
     return OP == G_DX ? p.n_in : OP == G_MM && ROWM ? rows : p.n_out;
   }
@@ -356,45 +359,46 @@ template <typename Tiles>
 struct GuWalk {
   const GmmProblem& p;
   const GuLine& l;
-  int pair, cols, n_tiles, whole;  // whole: tiles dealt whole to each pair
+  int pair, cols, n_tiles, whole, halves;  // whole, halves: tiles and half tiles dealt to each pair
   int row;
   long long begin, end;
 
-  MOE_DEV GuWalk(const GmmProblem& p_, const GuLine& l_, int pair_, int cols_, int n_tiles_, int whole_)
-      : p(p_), l(l_), pair(pair_), cols(cols_), n_tiles(n_tiles_), whole(whole_), row(0) {
+  MOE_DEV GuWalk(const GmmProblem& p_, const GuLine& l_, int pair_, int cols_, int n_tiles_, int whole_, int halves_)
+      : p(p_), l(l_), pair(pair_), cols(cols_), n_tiles(n_tiles_), whole(whole_), halves(halves_), row(0) {
     begin = l.cut[pair];
     end = l.cut[pair + 1];
-    if (whole == 0) seek();
+    if (whole + halves == 0) seek();
   }
+  // tiles (halves for MT = 2) on the line
+  MOE_DEV int on_line() const { return (n_tiles - whole * cols) * Tiles::MT - halves * cols; }
   // to the piece's first tile: the last one that begins at or before it
   MOE_DEV void seek() {
     if (begin == end) return;
-    int lo = 0, hi = (n_tiles - whole * cols) * Tiles::MT;
+    int lo = 0, hi = on_line();
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (l.tail[mid] <= begin) lo = mid;
       else hi = mid;
     }
-    row = whole + lo;
+    row = whole + halves + lo;
   }
   MOE_DEV bool next(GuItem& it) {
     for (;;) {
-      const bool dealt = row < whole;
-      const int t = row - whole;
-      if (!dealt && (begin >= end || t >= (n_tiles - whole * cols) * Tiles::MT || l.tail[t] >= end)) return false;
-      if (Tiles::MT == 1 || dealt) Tiles::get(p, l, dealt ? row * cols + pair : whole * cols + t, it);
-      else Tiles::get_tail(p, l, whole * cols, t, it);
+      const int t = row - whole - halves;
+      if (t >= 0 && (begin >= end || t >= on_line() || l.tail[t] >= end)) return false;
+      if (row < whole) Tiles::get(p, l, row * cols + pair, it);
+      else Tiles::get_tail(p, l, whole * cols, t < 0 ? (row - whole) * cols + pair : halves * cols + t, it);
       ++row;
       it.kb0 = 0;
       it.kb1 = it.nkb;
       it.pos = 0;
-      if (dealt) {
-        if (row == whole) seek();
-        return true;
+      if (t < 0) {
+        if (t == -1) seek();
+      } else {
+        it.pos = l.tail[t];
+        it.kb0 = steps_before(begin, it);
+        it.kb1 = steps_before(end, it);
       }
-      it.pos = l.tail[t];
-      it.kb0 = steps_before(begin, it);
-      it.kb1 = steps_before(end, it);
       if (it.kb0 < it.kb1) return true;
     }
   }
@@ -413,7 +417,8 @@ struct GuWalk {
 // caller's, and checked before any is used as an index: 0 <= off[0] <= ... <=
 // off[E] <= rows).
 template <int OP, typename Tiles, int NT>
-MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split_most, int* whole_out) {
+MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split_most, int* whole_out,
+                    int* halves_out) {
   const int warp = tid >> 5, lane = tid & 31;
   auto sync = [] {
     if constexpr (NT == 32) __syncwarp();
@@ -458,7 +463,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
     if (k > 0 && 32 * k + lane < p.E) l.cum[32 * k + lane] += before;
   }
   if (tid == 0) l.cum[p.E] = n_tiles;
-  const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, tails = (n_tiles - dealt) * Tiles::MT;
+  const int whole = max(0, n_tiles / cols - 1), dealt = whole * cols, rest = (n_tiles - dealt) * Tiles::MT;
   if constexpr (OP == G_DW)
     for (int i = tid; i < cols; i += NT) l.hand[i] = 0;
   sync();
@@ -477,10 +482,26 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[q]), (unsigned long long)c);
     }
   }
-  // the costs of the tiles that are split (at most kGuTailMost - 1 of them)
+  // What is left (halves of tiles for MT = 2; at most kGuTailMost - 1).  mm, dx,
+  // all of one length: as many as there are for every pair are dealt too, and
+  // each of the others is cut evenly for as many pairs as there are, unless
+  // the line is shorter in all (its sums to join cost as much as some 24
+  // steps, and pairs have two of them).
+  int halves = 0, each_in = 0;
+  if constexpr (OP != G_DW) {
+    const int steps = Tiles::steps(p, 0), q = rest / cols, r = rest - q * cols;
+    const int k = r ? min(split_most, cols / r) : 1;
+    const float even = q * steps + (r ? (float)steps / k : 0.f) + (k > 1 ? 24.f : 0.f);
+    const float line = (float)steps * rest / cols + 36.f;
+    if (even <= line) {
+      halves = q;
+      each_in = k;
+    }
+  }
+  const int tails = rest - halves * cols;
   for (int i = tid; i < tails; i += NT) {
     GuItem it;
-    Tiles::get_tail(p, l, dealt, i, it);
+    Tiles::get_tail(p, l, dealt, halves * cols + i, it);
     l.tail[i] = (long long)it.nkb * it.cost;
   }
   sync();
@@ -497,17 +518,19 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       if (i0 + lane < tails) l.tail[i0 + lane] = sum + y - v;
       sum += __shfl_sync(0xffffffffu, y, 31);
     }
-    if (OP != G_DW || whole == 0) {
+    if (lane == 0) l.tail[tails] = sum;
+    __syncwarp();
+    if (each_in) {
+      for (int i = lane; i <= cols; i += 32) {
+        const int t = i / each_in, part = i - t * each_in;
+        l.cut[i] = t < tails ? l.tail[t] + (l.tail[t + 1] - l.tail[t]) * part / each_in : sum;
+      }
+    } else if (OP != G_DW || whole == 0) {
       // Pieces of one length, a tile cut into split_most on average at most.
-      // Fewer tiles than pairs: a whole number of pieces per tile, so that a
-      // pair works on one tile, unless that leaves over a fifth of the pairs
-      // without work (one token over eight experts: 64 tiles whole, no sums
-      // to join, 128 SMs fill the memory's bandwidth as well as 148).
-      int pieces = max(1, (int)min((long long)cols, (long long)tails * split_most));
-      if (tails > 0 && tails < pieces && pieces / tails * tails * 5 >= pieces * 4) pieces = pieces / tails * tails;
+      const int pieces = max(1, (int)min((long long)cols, (long long)tails * split_most));
       const long long each = sum / pieces;
-      const int rest = (int)(sum - each * pieces);
-      for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * each + i * rest / pieces : sum;
+      const int over = (int)(sum - each * pieces);
+      for (int i = lane; i <= cols; i += 32) l.cut[i] = i < pieces ? i * each + i * over / pieces : sum;
     } else {
       // a piece brings its pair up to the mean of all pairs
       long long hands = 0;
@@ -532,10 +555,10 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       for (int i = lane; i < cols; i += 32) l.cut[i] = min(sum, (long long)((double)l.cut[i] * scale));
       if (lane == 0) l.cut[cols] = sum;
     }
-    if (lane == 0) l.tail[tails] = sum;
   }
   sync();
   *whole_out = whole;
+  *halves_out = halves;
   return n_tiles;
 }
 
@@ -766,13 +789,13 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   // The plan.  Only the item warp works from it (and the epilogue reads the
   // cuts, after an item), so it makes it while the others set up; with many
   // experts it takes the whole block (256 experts: 2.9 us, one warp 6.9).
-  int whole = 0, n_tiles = -1;
-  const bool by_block = OP == G_DW || g.E > 64;
-  if (by_block) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole);
+  int whole = 0, halves = 0, n_tiles = -1;
+  const bool by_block = OP == G_DW || MT > 1 || g.E > 64;
+  if (by_block) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole, &halves);
   tc_fence_before();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if constexpr (OP != G_DW)
-    if (!by_block && warp == 3) n_tiles = gu_plan<OP, Tiles, 32>(g, line, lane, cols, p.split_most, &whole);
+    if (!by_block && warp == 3) n_tiles = gu_plan<OP, Tiles, 32>(g, line, lane, cols, p.split_most, &whole, &halves);
   if (warp == 3 && lane == 0 && n_tiles < 0) {
     set_error(g.err, kErrDeviceInput);
     line.cut[pair] = line.cut[pair + 1] = 0;
@@ -856,23 +879,27 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                 for (int q = 0; q < panels; ++q) gu_tma_2d(b + q * 8192, &p.b_map[0], n + 64 * q, y, fb);
               }
             } else {
-              // Rows up to a multiple of 16: eight at a time while the expert
-              // has eight, then one by one to the next multiple of eight (those
-              // beyond the expert's from beyond the tensor, zeros), then eight
-              // zero rows if the multiple of 16 is not reached.
-              const int fill = (left + 15) & ~15, eights = left >> 3, ones = left & 7 ? 8 : 0;
-              const int zeros = fill - 8 * eights - ones > 0 ? 1 : 0, pieces = eights + ones + zeros;
+              // The rows that are left, and zeros (from beyond the tensor) up
+              // to a multiple of 16, each in boxes of their binary digits.
+              const int fill = (left + 15) & ~15, zeros = fill - left;
+              const int n_left = __popc(left), pieces = n_left + __popc(zeros);
               if (lane == 0 && leader) um_expect_tx(full(st), (uint32_t)(2 * fill * 128 * (a_panels + panels)));
               __syncwarp();
               for (int i = lane; i < pieces * (a_panels + panels); i += 32) {
                 const int q = i / pieces, w = i - q * pieces;
-                const bool one = w >= eights && w < eights + ones;
-                const int r = w < eights ? 8 * w : one ? 8 * eights + w - eights : 8 * eights + ones;
+                const bool zero = w >= n_left;
+                int digits = zero ? zeros : left, r = zero ? left : 0;
+                for (int k = zero ? w - n_left : w; k > 0; --k) {  // past the larger digits
+                  const int top = 31 - __clz(digits);
+                  digits ^= 1 << top;
+                  r += 1 << top;
+                }
+                const int size = 31 - __clz(digits);
                 const bool is_a = q < a_panels;
                 const uint32_t dst = (is_a ? a + q * 8192 : b + (q - a_panels) * 8192) + (uint32_t)(r * 128);
                 const CUtensorMap* maps = is_a ? p.a_tail : p.b_tail;
                 const int x = is_a ? m + 256 * (q >> 1) + 64 * (q & 1) : n + 64 * (q - a_panels);
-                gu_tma_2d(dst, &maps[one ? 1 : 0], x, r < left ? y + r : g.rows, fb);
+                gu_tma_2d(dst, &maps[5 - size], x, zero ? g.rows : y + r, fb);
               }
               __syncwarp();
             }
@@ -1060,7 +1087,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     } else {
       // ================= the items of this CTA, a few ahead of the warps that work on them
       if (lane == 0) {
-        Walk walk(g, line, (int)pair, cols, max(n_tiles, 0), whole);
+        Walk walk(g, line, (int)pair, cols, max(n_tiles, 0), whole, halves);
         GuItem it;
         int at = 0;
         uint32_t ph = 0;
@@ -1368,31 +1395,30 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         if (!ok) break;
         if (*flag) {
           __threadfence();
-          // SR rows at a time, four parts' loads in flight together
-          constexpr int Q = SR / 4;
+          // 32 columns at a time, two parts' loads in flight together
 #pragma unroll 1
-          for (int c = h; SR * c < it.nv; c += H) {
-            float v[SR];
+          for (int c = h; c < chunks; c += H) {
+            float v[32];
 #pragma unroll
-            for (int i = 0; i < SR; ++i) v[i] = 0.f;
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 1
             for (int from = first; from <= last; from += 32) {
               uint32_t left = with_part(from);
 #pragma unroll 1
               while (left) {
-                float4 a[4][Q];
+                float4 a[2][8];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < 2; ++s) {
                   const int piece = from + __ffs(left) - 1;
-                  const float4* src = part_of(max(piece, 0), piece == first ? 1 : 0) + Q * c * 128;
+                  const float4* src = part_of(max(piece, 0), piece == first ? 1 : 0) + 8 * c * 128;
 #pragma unroll
-                  for (int i = 0; i < Q; ++i) a[s][i] = left ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+                  for (int i = 0; i < 8; ++i) a[s][i] = left ? __ldcg(src + i * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
                   left &= left - 1;
                 }
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
+                for (int s = 0; s < 2; ++s)
 #pragma unroll
-                  for (int i = 0; i < Q; ++i) {
+                  for (int i = 0; i < 8; ++i) {
                     v[4 * i] += a[s][i].x;
                     v[4 * i + 1] += a[s][i].y;
                     v[4 * i + 2] += a[s][i].z;
@@ -1400,7 +1426,8 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
                   }
               }
             }
-            out_sr(c, v, 0);
+            out_sr(2 * c, v, 0);
+            out_sr(2 * c + 1, v, 16);
           }
         }
       }
