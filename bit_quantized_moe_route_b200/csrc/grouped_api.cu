@@ -96,10 +96,10 @@ moe_status_t check_gmm_ws(void* ws, size_t ws_bytes) {
 
 template <int OP, int IN>
 moe_status_t launch_any(const GmmProblem& p, cudaStream_t s, int sms) {
-  const long long m_tiles = ((OP == G_MM ? p.n_out : p.n_in) + kGaTile - 1) / kGaTile;
-  const long long n_tiles = OP == G_DW ? (long long)p.E * ((p.n_out + kGaTile - 1) / kGaTile)
-                                       : (p.rows + kGaTile - 1) / kGaTile + std::min(p.E, p.rows);
-  const int grid = (int)std::min<long long>(m_tiles * n_tiles, (long long)sms * 5);
+  const long long m_tiles = ((OP == G_MM ? p.n_out : p.n_in) + kGaM - 1) / kGaM;
+  const long long n_tiles = OP == G_DW ? (long long)p.E * ((p.n_out + kGaN - 1) / kGaN)
+                                       : (p.rows + kGaN - 1) / kGaN + std::min(p.E, p.rows);
+  const int grid = (int)std::min<long long>(m_tiles * n_tiles, 2LL * sms);
   grouped_any_kernel<OP, IN><<<grid, kGaThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "grouped_any_kernel: %s", cudaGetErrorString(e));
