@@ -6,7 +6,6 @@
 #include <atomic>
 
 #include "api_util.h"
-#include "grouped_any.cuh"
 #include "grouped_umma.cuh"
 #include "quant_fp8.cuh"
 
@@ -94,27 +93,15 @@ moe_status_t check_gmm_ws(void* ws, size_t ws_bytes) {
   return api_check_dev_ptr(ws, "workspace");
 }
 
-template <int OP, int IN>
-moe_status_t launch_any(const GmmProblem& p, cudaStream_t s, int sms) {
-  const long long m_tiles = ((OP == G_MM ? p.n_out : p.n_in) + kGaM - 1) / kGaM;
-  const long long n_tiles = OP == G_DW ? (long long)p.E * ((p.n_out + kGaN - 1) / kGaN)
-                                       : (p.rows + kGaN - 1) / kGaN + std::min(p.E, p.rows);
-  const int grid = (int)std::min<long long>(m_tiles * n_tiles, 2LL * sms);
-  grouped_any_kernel<OP, IN><<<grid, kGaThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return api_fail(MOE_ERR_CUDA, "grouped_any_kernel: %s", cudaGetErrorString(e));
-  return MOE_OK;
-}
-
 // Resident pairs of a tensor-memory kernel on the current device (0: none).
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
 int resident_pairs() {
   static std::atomic<int> cached[64];  // pairs + 1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = cached[dev].load(std::memory_order_acquire);
   if (!v) {
-    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN>() + 1;
+    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>() + 1;
     cached[dev].store(v, std::memory_order_release);
   }
   return v - 1;
@@ -122,55 +109,53 @@ int resident_pairs() {
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// TMA's rules: base addresses and row strides in multiples of 16 bytes; and
-// an expert's steps have to fit 32 bits.
+// TMA's rules: base addresses and row strides in multiples of 16 bytes.
 template <int OP>
-bool umma_ok(const GmmProblem& p, int es) {
+bool tma_ok(const GmmProblem& p, int es) {
   if (p.rows < 1 || !aligned16(p.rows_in) || p.ld_rows * es % 16) return false;
-  if (OP == G_DW ? !aligned16(p.x) || p.ld_x * es % 16 : !aligned16(p.w) || (long long)p.n_in * es % 16) return false;
-  const long long n = OP == G_DW ? p.n_in : p.rows, m = OP == G_DX ? p.n_in : p.n_out;
-  const long long k = OP == G_MM ? p.n_in : OP == G_DX ? p.n_out : p.rows;
-  return (n / 128 + 1) * (m / 256 + 1) * (k / 64 + 1) < (1LL << 31);
+  return OP == G_DW ? aligned16(p.x) && p.ld_x * es % 16 == 0 : aligned16(p.w) && (long long)p.n_in * es % 16 == 0;
 }
 
 // The 8-bit product has its rows on the M side from this mean per expert on.
 constexpr long long kRowsPerExpertM = 192;
 
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
-  const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN>();
+  const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>();
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
-  const uint64_t es = FP8 ? 1 : 2;
-  const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : type == G_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const uint32_t inner = 128 / es;
   GuParams q;
   q.g = p;
   q.type = type;
   q.ws = reinterpret_cast<unsigned char*>(ws);
   q.split_most = 16;
-  if constexpr (OP == G_DW) {
-    const uint64_t dims_x[2] = {(uint64_t)p.n_in, (uint64_t)p.rows}, st_x[1] = {(uint64_t)p.ld_x * es};
-    const uint64_t dims_y[2] = {(uint64_t)p.n_out, (uint64_t)p.rows}, st_y[1] = {(uint64_t)p.ld_rows * es};
-    for (int i = 0; i < 7; ++i) {
-      const uint32_t box[2] = {inner, 64u >> i};
-      GMM_TRY(api_tensor_map(i ? &q.a_tail[i - 1] : &q.a_map, dt, 2, p.rows_in, dims_y, st_y, box));
-      GMM_TRY(api_tensor_map(i ? &q.b_tail[i - 1] : &q.b_map[0], dt, 2, p.x, dims_x, st_x, box));
-    }
-  } else {
-    const uint64_t dims_w[3] = {(uint64_t)p.n_in, (uint64_t)p.n_out, (uint64_t)p.E};
-    const uint64_t st_w[2] = {(uint64_t)p.n_in * es, (uint64_t)p.n_in * p.n_out * es};
-    const uint32_t box_w[3] = {inner, OP == G_MM ? 128u : 64u, 1u};
-    GMM_TRY(api_tensor_map(ROWM ? &q.b_map[0] : &q.a_map, dt, 3, p.w, dims_w, st_w, box_w));
-    const uint64_t dims_r[2] = {(uint64_t)(OP == G_MM ? p.n_in : p.n_out), (uint64_t)p.rows};
-    const uint64_t st_r[1] = {(uint64_t)p.ld_rows * es};
-    // no tile has more rows than there are: boxes beyond the first that holds half of them are not used
-    for (int i = ROWM ? 3 : 0; i < 4 && (ROWM || i == 0 || p.rows > (32 << (i - 1))); ++i) {
-      const uint32_t box[2] = {inner, 16u << i};
-      GMM_TRY(api_tensor_map(ROWM ? &q.a_map : &q.b_map[i], dt, 2, p.rows_in, dims_r, st_r, box));
+  if constexpr (!LDG) {
+    const uint64_t es = FP8 ? 1 : 2;
+    const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                       : type == G_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint32_t inner = 128 / es;
+    if constexpr (OP == G_DW) {
+      const uint64_t dims_x[2] = {(uint64_t)p.n_in, (uint64_t)p.rows}, st_x[1] = {(uint64_t)p.ld_x * es};
+      const uint64_t dims_y[2] = {(uint64_t)p.n_out, (uint64_t)p.rows}, st_y[1] = {(uint64_t)p.ld_rows * es};
+      for (int i = 0; i < 7; ++i) {
+        const uint32_t box[2] = {inner, 64u >> i};
+        GMM_TRY(api_tensor_map(i ? &q.a_tail[i - 1] : &q.a_map, dt, 2, p.rows_in, dims_y, st_y, box));
+        GMM_TRY(api_tensor_map(i ? &q.b_tail[i - 1] : &q.b_map[0], dt, 2, p.x, dims_x, st_x, box));
+      }
+    } else {
+      const uint64_t dims_w[3] = {(uint64_t)p.n_in, (uint64_t)p.n_out, (uint64_t)p.E};
+      const uint64_t st_w[2] = {(uint64_t)p.n_in * es, (uint64_t)p.n_in * p.n_out * es};
+      const uint32_t box_w[3] = {inner, OP == G_MM ? 128u : 64u, 1u};
+      GMM_TRY(api_tensor_map(ROWM ? &q.b_map[0] : &q.a_map, dt, 3, p.w, dims_w, st_w, box_w));
+      const uint64_t dims_r[2] = {(uint64_t)(OP == G_MM ? p.n_in : p.n_out), (uint64_t)p.rows};
+      const uint64_t st_r[1] = {(uint64_t)p.ld_rows * es};
+      // no tile has more rows than there are: boxes beyond the first that holds half of them are not used
+      for (int i = ROWM ? 3 : 0; i < 4 && (ROWM || i == 0 || p.rows > (32 << (i - 1))); ++i) {
+        const uint32_t box[2] = {inner, 16u << i};
+        GMM_TRY(api_tensor_map(ROWM ? &q.a_map : &q.b_map[i], dt, 2, p.rows_in, dims_r, st_r, box));
+      }
     }
   }
-  if (!gu_launch<OP, FP8, ROWM, MT, CHAIN>(q, pairs, s))
+  if (!gu_launch<OP, FP8, ROWM, MT, CHAIN, LDG>(q, pairs, s))
     return api_fail(MOE_ERR_CUDA, "grouped_umma_kernel: %s", cudaGetErrorString(cudaGetLastError()));
   return MOE_OK;
 }
@@ -187,21 +172,20 @@ bool many_tiles(const GmmProblem& p) {
 
 template <int OP>
 moe_status_t run_gmm(const GmmProblem& p, int in_type, void* ws, cudaStream_t s) {
-  if (umma_ok<OP>(p, in_type == G_E4M3 ? 1 : 2)) {
+  constexpr bool ROWM = OP == G_DW;
+  const bool fp8 = in_type == G_E4M3;
+  if (!tma_ok<OP>(p, fp8 ? 1 : 2)) {
     if constexpr (OP == G_MM)
-      if (in_type == G_E4M3)
-        return (long long)p.rows >= kRowsPerExpertM * p.E ? launch_umma<OP, true, true, 1, 1>(p, in_type, ws, s)
-                                                          : launch_umma<OP, true, false, 1, 1>(p, in_type, ws, s);
-    if (p.out_type == G_FP32) return launch_umma<OP, false, OP == G_DW, 1, kGuChain>(p, in_type, ws, s);
-    return many_tiles<OP>(p) ? launch_umma<OP, false, OP == G_DW, 2, 0>(p, in_type, ws, s)
-                             : launch_umma<OP, false, OP == G_DW, 1, 0>(p, in_type, ws, s);
+      if (fp8) return launch_umma<OP, true, false, 1, 1, true>(p, in_type, ws, s);
+    return launch_umma<OP, false, ROWM, 1, 0, true>(p, in_type, ws, s);
   }
-  int sms = 0;
-  if (sm_count(&sms)) return api_fail(MOE_ERR_CUDA, "device query failed");
-  if (in_type == G_BF16) return launch_any<OP, G_BF16>(p, s, sms);
-  if (in_type == G_FP16) return launch_any<OP, G_FP16>(p, s, sms);
-  if constexpr (OP == G_MM) return launch_any<OP, G_E4M3>(p, s, sms);
-  return api_fail(MOE_ERR_UNSUPPORTED, "type");
+  if constexpr (OP == G_MM)
+    if (fp8)
+      return (long long)p.rows >= kRowsPerExpertM * p.E ? launch_umma<OP, true, true, 1, 1, false>(p, in_type, ws, s)
+                                                        : launch_umma<OP, true, false, 1, 1, false>(p, in_type, ws, s);
+  if (p.out_type == G_FP32) return launch_umma<OP, false, ROWM, 1, kGuChain, false>(p, in_type, ws, s);
+  return many_tiles<OP>(p) ? launch_umma<OP, false, ROWM, 2, 0, false>(p, in_type, ws, s)
+                           : launch_umma<OP, false, ROWM, 1, 0, false>(p, in_type, ws, s);
 }
 
 // The products over rows: mm (rows_in = x) and dx (rows_in = dy).

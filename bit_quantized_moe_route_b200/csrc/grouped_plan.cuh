@@ -1,5 +1,4 @@
-// What the grouped products share: their parameters and the walk over the
-// experts' row ranges.
+// What the grouped products share: their parameters.
 //
 // Rows are in expert order, expert e owning rows [off[e], off[e+1]):
 //   mm   y[r, o]     = sum_i W[e, o, i] x[r, i]
@@ -10,6 +9,8 @@
 // its rows (r, r, o), so that one epilogue serves all three and an expert with
 // few rows costs a narrow N instead of a padded M.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -41,55 +42,6 @@ MOE_DEV void gmm_store(void* out, int type, long long i, float v) {
   if (type == G_BF16) reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
   else if (type == G_FP16) reinterpret_cast<__half*>(out)[i] = __float2half_rn(v);
   else reinterpret_cast<float*>(out)[i] = v;
-}
-
-// Called by every thread of the block: cum[e] = work units of the experts
-// before e, for units(rows of the expert) units each, and cum[E] the total.
-// The offsets are the caller's, so they are checked here, before any of them
-// is used as an index: 0 <= off[0] <= ... <= off[E] <= rows.  Returns false
-// (in every thread, with the error recorded) when they are not.
-template <typename Units>
-MOE_DEV bool gmm_plan(const GmmProblem& p, Units units, long long* cum, int* flag) {
-  if (threadIdx.x == 0) *flag = 1;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    long long base = 0;
-    bool ok = true;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      long long u = 0;
-      if (e < p.E) {
-        const int a = gmm_off(p, e), b = gmm_off(p, e + 1);
-        if (a < 0 || b < a || b > p.rows) ok = false;
-        else u = units(b - a);
-      }
-      long long s = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (e < p.E) cum[e] = base + s - u;
-      base += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (lane == 0) cum[p.E] = base;
-    if (!ok) *flag = 0;
-  }
-  __syncthreads();
-  if (!*flag && threadIdx.x == 0) set_error(p.err, kErrDeviceInput);
-  return *flag != 0;
-}
-
-// The expert whose units hold unit u (0 <= u < cum[E]).
-MOE_DEV int gmm_expert_of(const long long* cum, int E, long long u) {
-  int lo = 0, hi = E;  // cum[lo] <= u < cum[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= u) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 }  // namespace moe

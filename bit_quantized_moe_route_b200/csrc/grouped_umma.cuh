@@ -34,6 +34,13 @@
 // comes from beyond the tensor's end, which TMA fills with zeros, so that no
 // value of another expert's rows (a NaN, say) enters a product.
 //
+// LDG: operands of any alignment and row stride, which TMA cannot read.  Eight
+// more warps bring each step in: a 16-byte piece at any address is cut out of
+// the two aligned 16-byte blocks that hold it (both inside the operand, else
+// byte by byte) and stored where TMA would have put it; values beyond the
+// matrix or the expert's rows are zeros.  Bound by those loads' latency and
+// the instructions around them.
+//
 // The tiles, in the order expert, M tile, row tile, are dealt out to the pairs
 // of CTAs in turn, so that pairs that run at the same time read the same
 // weights and rows from L2 (with each pair on a run of neighbouring tiles
@@ -88,8 +95,15 @@ constexpr int kGuStageRows = 16;          // output rows that a warp stores toge
 // Registers per thread at launch and, where the epilogue holds a tile's sums or
 // rounded outputs, then of warps 0-3 and of the epilogue.
 constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
+// LDG: eight more warps; less for each.
+constexpr int kGuLoadWarps = 8;
+constexpr int gu_threads(bool ldg) { return kGuThreads + (ldg ? 32 * kGuLoadWarps : 0); }
+constexpr int kGuLdgRegs = 96, kGuLdgLow = 64, kGuLdgHigh = 112;  // (the load warps keep theirs)
+static_assert(128 * kGuLdgLow + 32 * kGuLoadWarps * kGuLdgRegs + 32 * kGuEpiWarps * kGuLdgHigh <= gu_threads(true) * kGuLdgRegs,
+              "registers of the block");
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
+constexpr int gu_launch_regs(bool ldg) { return ldg ? kGuLdgRegs : kGuRegs; }
 constexpr int kGuScaleSlots = 5;
 constexpr int kGuScaleAhead = 4;          // slots whose copies are in flight
 constexpr int kGuItems = 4;               // items handed out ahead
@@ -230,6 +244,55 @@ MOE_DEV void gu_times(unsigned long long (&acc)[16], const int c0, const uint32_
   for (int i = 0; i < 16; i += 2) gu_fma2(acc[(c0 + i) / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
 }
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
+// LDG: a 16-byte piece on its way, n valid bytes from p on, of an operand
+// whose bytes are [lo, hi).
+struct GuPiece {
+  uint4 a, b;
+  MOE_DEV void load(const char* p, int n, const char* lo, const char* hi) {
+    if (n <= 0) return;
+    const char* p0 = p - (reinterpret_cast<uintptr_t>(p) & 15);
+    if (p0 >= lo && p0 + 32 <= hi) {
+      a = __ldg(reinterpret_cast<const uint4*>(p0));
+      b = __ldg(reinterpret_cast<const uint4*>(p0) + 1);
+    } else {  // at an end of the operand
+      unsigned long long w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = 0;
+#pragma unroll 1
+        for (int i = 7; i >= 0; --i) {
+          const char* q = p0 + 8 * k + i;
+          w[k] = w[k] << 8 | (q >= lo && q < hi ? *reinterpret_cast<const uint8_t*>(q) : 0u);
+        }
+      }
+      a = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+      b = make_uint4((uint32_t)w[2], (uint32_t)(w[2] >> 32), (uint32_t)w[3], (uint32_t)(w[3] >> 32));
+    }
+  }
+  // shift: p's last four bits
+  MOE_DEV void store(uint32_t to, int n, uint32_t shift) const {
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (n > 0) {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t t[6], u[5];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) t[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) u[i] = shift & 4 ? t[i + 1] : t[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], (shift & 3) * 8);
+      if (n < 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int left = n - 4 * i;  // valid bytes of this word
+          o[i] = left >= 4 ? o[i] : left <= 0 ? 0u : o[i] & (0xFFFFFFFFu >> (32 - 8 * left));
+        }
+      }
+    }
+    tc_sts128(to, o[0], o[1], o[2], o[3]);
+  }
+};
+
 // ------------------------------------------------------------ work items
 // A run of steps of one tile.
 struct alignas(16) GuItem {
@@ -470,8 +533,8 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   // What each pair's whole tiles cost.  mm, dx: as good as the same for all
   // pairs.  dw: a tile's steps are its expert's rows.
   if constexpr (OP == G_DW) {
-    const int q = tid % 96, part = tid / 96;
-    if (whole > 0 && q < cols) {
+    const int q = tid % 96, part = tid / 96;  // (threads beyond a multiple of 96 have no part)
+    if (whole > 0 && q < cols && part < NT / 96) {
       long long c = 0;
       for (int e = part; e < p.E; e += NT / 96) {
         const int g0 = min(l.cum[e], dealt), g1 = min(l.cum[e + 1], dealt);
@@ -711,12 +774,14 @@ MOE_DEV void gu_row_out16(void* out, long long base, int left, int unit, const u
 
 // ------------------------------------------------------------ the kernel
 // Launched in clusters of two CTAs (gridDim.x even), one CTA per SM.
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
-__global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __grid_constant__ GuParams p) {
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
+__global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const __grid_constant__ GuParams p) {
   constexpr int EW = kGuEpiWarps, H = EW / 4, SR = kGuStageRows;
   constexpr bool SCALE_RING = FP8 && !ROWM;  // the scales come through shared memory
   static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
-  static_assert(MT == 1 || CHAIN == 0, "register sums hold one MMA's");
+  static_assert(MT == 1 || (CHAIN == 0 && !LDG), "register sums and loads hold one MMA's");
+  // what the kernel knows of the output's type: 1 fp32, 0 16 bits, -1 nothing
+  constexpr int F32 = FP8 || LDG ? -1 : CHAIN ? 1 : 0;
   constexpr int NS = 12 / (MT + 1);           // stages
   constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
   using Tiles = GuTiles<OP, FP8, ROWM, MT>;
@@ -759,7 +824,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      tc_bar_init(full(s), 1);
+      tc_bar_init(full(s), LDG ? 2 * kGuLoadWarps : 1);
       tc_bar_init(empty(s), 1);
     }
     for (int b = 0; b < kGuSegs; ++b) {
@@ -772,7 +837,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
     }
     for (int s = 0; s < kGuItems; ++s) {
       tc_bar_init(it_full(s), 1);
-      tc_bar_init(it_empty(s), 1 + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
+      tc_bar_init(it_empty(s), (LDG ? kGuLoadWarps : 1) + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
     }
     tc_bar_init(drain, 1);
     tc_bar_init(join, EW);
@@ -791,7 +856,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
   // experts it takes the whole block (256 experts: 2.9 us, one warp 6.9).
   int whole = 0, halves = 0, n_tiles = -1;
   const bool by_block = OP == G_DW || MT > 1 || g.E > 64;
-  if (by_block) n_tiles = gu_plan<OP, Tiles, kGuThreads>(g, line, tid, cols, p.split_most, &whole, &halves);
+  if (by_block) n_tiles = gu_plan<OP, Tiles, gu_threads(LDG)>(g, line, tid, cols, p.split_most, &whole, &halves);
   tc_fence_before();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if constexpr (OP != G_DW)
@@ -831,8 +896,11 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
 
   if (warp < 4) {
     // the epilogue gets registers of these warps (the host checks that the block has kGuRegs per thread)
-    if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
-    if (warp == 0) {
+    if constexpr (LDG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLow));
+    else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
+    if (LDG && warp == 0) {
+      // (the load warps bring the operands)
+    } else if (warp == 0) {
       // ================= TMA issuer of this CTA's halves of both operands
       // (lane 0; all lanes share the many small copies of dw's last steps)
       if (lane == 0) {
@@ -1102,8 +1170,95 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
       }
       __syncwarp();
     }
+  } else if (LDG && warp >= 4 + kGuEpiWarps) {
+    if constexpr (LDG) {
+      // ================= loads of any alignment: A and B of each step, four
+      // pieces of each per thread
+      constexpr int ES = FP8 ? 1 : 2;
+      const int lt = tid - kGuThreads;  // 0 .. 255
+      const char* w_lo = reinterpret_cast<const char*>(g.w);
+      const char* w_hi = w_lo + (long long)g.E * g.n_out * g.n_in * ES;
+      const char* r_lo = reinterpret_cast<const char*>(g.rows_in);
+      const char* r_hi = r_lo + ((long long)(g.rows - 1) * g.ld_rows + (OP == G_MM ? g.n_in : g.n_out)) * ES;
+      const char* x_lo = reinterpret_cast<const char*>(g.x);
+      const char* x_hi = x_lo + ((long long)(g.rows - 1) * g.ld_x + g.n_in) * ES;
+      // K-major: row (lt >> 3) + 32 j, 16-byte piece lt & 7 of the step's 128
+      // bytes; `rows` there are, `len` bytes left of each
+      auto k_major = [&](uint32_t dst, const char* p, long long ld, int rows, int len, const char* lo, const char* hi) {
+        const int c = lt & 7, r0 = lt >> 3;
+        GuPiece v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = r0 + 32 * j;
+          v[j].load(p + r * ld + 16 * c, r < rows ? min(16, len - 16 * c) : 0, lo, hi);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = r0 + 32 * j;
+          v[j].store(dst + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)), r < rows ? min(16, len - 16 * c) : 0,
+                     ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)ld) & 15u);
+        }
+      };
+      // M- or N-major: contracted row (lt >> 4) + 16 j of 64, piece lt & 15 of
+      // 256 bytes of values (two panels); `rows` there are, `len` bytes of each
+      auto mn_major = [&](uint32_t dst, const char* p, long long ld, int rows, int len, const char* lo, const char* hi) {
+        const int c = lt & 15, r0 = lt >> 4;
+        GuPiece v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = r0 + 16 * j;
+          v[j].load(p + r * ld + 16 * c, r < rows ? min(16, len - 16 * c) : 0, lo, hi);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = r0 + 16 * j;
+          v[j].store(dst + (uint32_t)((c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                     r < rows ? min(16, len - 16 * c) : 0,
+                     ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)ld) & 15u);
+        }
+      };
+      GuItem it;
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      while (ok && copy_item(it, false)) {
+        if (it.kind == GU_ZEROS) continue;
+        const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
+        const int mv = min(128, it.mv - (int)rank * 128), nv = min(half, it.nv - (int)rank * half);
+        const char* we = w_lo + (long long)it.e * g.n_out * g.n_in * ES;
+        const long long ldw = (long long)g.n_in * ES, ldr = g.ld_rows * ES, ldx = g.ld_x * ES;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
+          if (!ok) break;
+          const uint32_t a = base + (uint32_t)(st * kStep), b = a + kGuTile;
+          const int k0 = kb * KE;
+          if constexpr (OP == G_MM) {
+            const int len = (g.n_in - k0) * ES;
+            if constexpr (ROWM) {
+              k_major(a, r_lo + m * ldr + k0 * ES, ldr, mv, len, r_lo, r_hi);
+              k_major(b, we + n * ldw + k0 * ES, ldw, nv, len, w_lo, w_hi);
+            } else {
+              k_major(a, we + m * ldw + k0 * ES, ldw, mv, len, w_lo, w_hi);
+              k_major(b, r_lo + n * ldr + k0 * ES, ldr, nv, len, r_lo, r_hi);
+            }
+          } else if constexpr (OP == G_DX) {
+            mn_major(a, we + k0 * ldw + m * ES, ldw, g.n_out - k0, mv * ES, w_lo, w_hi);
+            k_major(b, r_lo + n * ldr + k0 * ES, ldr, nv, (g.n_out - k0) * ES, r_lo, r_hi);
+          } else {
+            const int left = it.r1 - it.r0 - k0;
+            mn_major(a, r_lo + (long long)(it.r0 + k0) * ldr + m * ES, ldr, left, mv * ES, r_lo, r_hi);
+            mn_major(b, x_lo + (long long)(it.r0 + k0) * ldx + n * ES, ldx, left, nv * ES, x_lo, x_hi);
+          }
+          tc_fence_proxy();  // the stores, before the tensor core reads them
+          __syncwarp();
+          if (lane == 0) cl_arrive(cl_addr(full(st), 0));
+          if (++st == NS) st = 0, ph ^= 1u;
+        }
+      }
+    }
   } else {
-    if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
+    if constexpr (LDG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuLdgHigh));
+    else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every H-th 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t buf = base + kGuOutOff + (uint32_t)((warp - 4) * SR * 128);
@@ -1145,12 +1300,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         const int left = it.nv - SR * c;
         if (left <= 0 || vals <= 0) return;
         if constexpr (ROWM) {
-          if (lane < vals) gu_row_out<SR, FP8 ? -1 : CHAIN ? 1 : 0>(g.out, g.out_type, ob + SR * c, left, unit, &v[at]);
+          if (lane < vals) gu_row_out<SR, F32>(g.out, g.out_type, ob + SR * c, left, unit, &v[at]);
         } else {
 #pragma unroll
           for (int i = 0; i < SR; ++i)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[at + i]) : "memory");
-          gu_rows_out<FP8 ? -1 : CHAIN ? 1 : 0>(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
+          gu_rows_out<F32>(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
         }
       };
       auto put = [&](int c, const float (&v)[32]) {  // N values 32 c ..
@@ -1187,7 +1342,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
         if (lane == 0) cl_arrive(cl_addr(acc_empty(seg & (kGuSegs - 1)), 0));
       };
       if constexpr (CHAIN == 0) {
-        if (all) {
+        if (!LDG && all) {
           // Rounded to the output's 16 bits on the way into registers, both
           // halves, so that the accumulators are free before the first store:
           // the next tile's MMAs wait for 800 clocks of TMEM reads then, and
@@ -1445,27 +1600,31 @@ __global__ void __launch_bounds__(kGuThreads, 1) grouped_umma_kernel(const __gri
 // One translation unit per kernel: gu_launch starts `pairs` clusters, gu_pairs
 // sets the kernel's attributes on the current device and returns how many
 // pairs fit at once (0: none).
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
 bool gu_launch(const GuParams& p, int pairs, cudaStream_t s);
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
 int gu_pairs();
 constexpr int kGuChain = 8;  // 16-bit products with fp32 outputs: 512 contracted values per chain
-#define MOE_GU_DECL(OP, FP8, ROWM, MT, CHAIN)                                             \
-  template <>                                                                             \
-  bool gu_launch<OP, FP8, ROWM, MT, CHAIN>(const GuParams& p, int pairs, cudaStream_t s); \
-  template <>                                                                             \
-  int gu_pairs<OP, FP8, ROWM, MT, CHAIN>();
-MOE_GU_DECL(G_MM, false, false, 1, 0)
-MOE_GU_DECL(G_MM, false, false, 2, 0)
-MOE_GU_DECL(G_MM, false, false, 1, kGuChain)
-MOE_GU_DECL(G_DX, false, false, 1, 0)
-MOE_GU_DECL(G_DX, false, false, 2, 0)
-MOE_GU_DECL(G_DX, false, false, 1, kGuChain)
-MOE_GU_DECL(G_DW, false, true, 1, 0)
-MOE_GU_DECL(G_DW, false, true, 2, 0)
-MOE_GU_DECL(G_DW, false, true, 1, kGuChain)
-MOE_GU_DECL(G_MM, true, false, 1, 1)
-MOE_GU_DECL(G_MM, true, true, 1, 1)
+#define MOE_GU_DECL(OP, FP8, ROWM, MT, CHAIN, LDG)                                             \
+  template <>                                                                                  \
+  bool gu_launch<OP, FP8, ROWM, MT, CHAIN, LDG>(const GuParams& p, int pairs, cudaStream_t s); \
+  template <>                                                                                  \
+  int gu_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>();
+MOE_GU_DECL(G_MM, false, false, 1, 0, false)
+MOE_GU_DECL(G_MM, false, false, 2, 0, false)
+MOE_GU_DECL(G_MM, false, false, 1, kGuChain, false)
+MOE_GU_DECL(G_MM, false, false, 1, 0, true)
+MOE_GU_DECL(G_DX, false, false, 1, 0, false)
+MOE_GU_DECL(G_DX, false, false, 2, 0, false)
+MOE_GU_DECL(G_DX, false, false, 1, kGuChain, false)
+MOE_GU_DECL(G_DX, false, false, 1, 0, true)
+MOE_GU_DECL(G_DW, false, true, 1, 0, false)
+MOE_GU_DECL(G_DW, false, true, 2, 0, false)
+MOE_GU_DECL(G_DW, false, true, 1, kGuChain, false)
+MOE_GU_DECL(G_DW, false, true, 1, 0, true)
+MOE_GU_DECL(G_MM, true, false, 1, 1, false)
+MOE_GU_DECL(G_MM, true, true, 1, 1, false)
+MOE_GU_DECL(G_MM, true, false, 1, 1, true)
 #undef MOE_GU_DECL
 
 }  // namespace moe

@@ -4,4 +4,5 @@
 #define GU_ROWM false
 #define GU_MT 2
 #define GU_CHAIN 0
+#define GU_LDG false
 #include "gu_inst.inl"

@@ -1,14 +1,16 @@
 // Instantiation unit of the grouped tensor-memory kernel (GU_OP, GU_FP8,
-// GU_ROWM, GU_MT, GU_CHAIN set by the including file).
+// GU_ROWM, GU_MT, GU_CHAIN, GU_LDG set by the including file).
 #include "grouped_umma.cuh"
 
 namespace moe {
 
 namespace {
+const auto gu_kernel = grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>;
+
 cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(kGuThreads);
+  cfg.blockDim = dim3(gu_threads(GU_LDG));
   cfg.dynamicSmemBytes = gu_smem();
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -22,30 +24,30 @@ cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* att
 }  // namespace
 
 template <>
-bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>(const GuParams& p, int pairs, cudaStream_t s) {
+bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>(const GuParams& p, int pairs, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
-  return cudaLaunchKernelEx(&cfg, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, p) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, gu_kernel, p) == cudaSuccess;
 }
 
 template <>
-int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>() {
-  if (cudaFuncSetAttribute(grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)gu_smem()) != cudaSuccess) {
+int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>() {
+  if (cudaFuncSetAttribute(gu_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gu_smem()) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   // the register hand-over of these kernels counts on what the block starts with
   cudaFuncAttributes fa;
-  if (gu_hand_over(GU_MT, GU_CHAIN) && (cudaFuncGetAttributes(&fa, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>) != cudaSuccess ||
-                       (fa.numRegs + 7) / 8 * 8 != kGuRegs)) {
-    cudaGetLastError();
-    return 0;
+  if (GU_LDG || gu_hand_over(GU_MT, GU_CHAIN)) {
+    if (cudaFuncGetAttributes(&fa, gu_kernel) != cudaSuccess || (fa.numRegs + 7) / 8 * 8 != gu_launch_regs(GU_LDG)) {
+      cudaGetLastError();
+      return 0;
+    }
   }
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, gu_kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
