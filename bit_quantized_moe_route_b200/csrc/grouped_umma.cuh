@@ -238,10 +238,10 @@ MOE_DEV void gu_scaled(unsigned long long (&acc)[16], const int c0, const uint32
     gu_fma2(acc[(c0 + i) / 2 + 1], gu_pack(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), s.y);
   }
 }
-// 16 step sums times one scale (in both halves of `s`)
-MOE_DEV void gu_times(unsigned long long (&acc)[16], const int c0, const uint32_t (&r)[16], unsigned long long s) {
+// 32 step sums times one scale (in both halves of `s`)
+MOE_DEV void gu_times(unsigned long long (&acc)[16], const uint32_t (&r)[32], unsigned long long s) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) gu_fma2(acc[(c0 + i) / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
+  for (int i = 0; i < 32; i += 2) gu_fma2(acc[i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
 }
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
 // LDG: a 16-byte piece on its way, n valid bytes from p on, of an operand
@@ -851,6 +851,12 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   const int cols = (int)npairs;
+  // Everything above is this CTA's own.  From here on global memory is read:
+  // the kernel before in the stream has to be through (launched with
+  // programmatic serialization, this one starts on SMs that it has left).
+  pdl_wait();
+  pdl_trigger();
+
   // The plan.  Only the item warp works from it (and the epilogue reads the
   // cuts, after an item), so it makes it while the others set up; with many
   // experts it takes the whole block (256 experts: 2.9 us, one warp 6.9).
@@ -1077,9 +1083,11 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             const int stride = SCALE_RING ? gu_stride(it.np) : kGuN;
             const int kend = SCALE_RING ? min(it.kb1, kb + kGuN / stride) : CHAIN ? min(it.kb1, kb + CHAIN) : it.kb1;
             uint32_t d, acc = 0;
-            ok = open_sum(FP8 ? kGuN : it.np, d);
-            for (; ok && kb < kend; ++kb) {
-              ok = cl_bar_wait(full(st), ph, abort_flag);
+            // (the operands are there before a hand-over's accumulator is: waited for first, their wait is hidden)
+            if (FP8) ok = cl_bar_wait(full(st), ph, abort_flag);
+            ok = ok && open_sum(FP8 ? kGuN : it.np, d);
+            for (const int first = kb; ok && kb < kend; ++kb) {
+              if (!FP8 || kb > first) ok = cl_bar_wait(full(st), ph, abort_flag);
               if (!ok) break;
               tc_fence_after();
               step_mma(st, 0, kb, d, idesc, acc);
@@ -1465,21 +1473,22 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             ok = wait_sums();
             if (!ok) break;
             const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
-            // columns 64 j + 32 h, j = 0..3, half of them at a time (those
-            // beyond the tile's hold what was there before and are not stored)
-            uint32_t r0[16], r1[16];
+            // columns 64 j + 32 h, j = 0..3 (those beyond the tile's hold what
+            // was there before and are not stored)
+            uint32_t r0[32], r1[32];
             gu_ld_issue(ta, r0);
             gu_ld_wait(r0);
-#pragma unroll
-            for (int t = 0; t < 8; t += 2) {
-              gu_ld_issue(ta + (uint32_t)(64 * (t / 2) + 16), r1);
-              gu_times(acc[t / 2], 0, r0, t < 4 ? s0 : s1);
-              gu_ld_wait(r1);
-              if (t < 6) gu_ld_issue(ta + (uint32_t)(64 * (t / 2 + 1)), r0);
-              else give_back();
-              gu_times(acc[t / 2], 16, r1, t < 4 ? s0 : s1);
-              if (t < 6) gu_ld_wait(r0);
-            }
+            gu_ld_issue(ta + 64, r1);
+            gu_times(acc[0], r0, s0);
+            gu_ld_wait(r1);
+            gu_ld_issue(ta + 128, r0);
+            gu_times(acc[1], r1, s0);
+            gu_ld_wait(r0);
+            gu_ld_issue(ta + 192, r1);
+            gu_times(acc[2], r0, s1);
+            gu_ld_wait(r1);
+            give_back();
+            gu_times(acc[3], r1, s1);
             ++seg;
           }
         } else {

@@ -17,15 +17,17 @@ cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* att
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 }  // namespace
 
 template <>
 bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>(const GuParams& p, int pairs, cudaStream_t s) {
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
   return cudaLaunchKernelEx(&cfg, gu_kernel, p) == cudaSuccess;
 }
@@ -44,7 +46,7 @@ int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>() {
       return 0;
     }
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, gu_kernel, &cfg) != cudaSuccess) {
