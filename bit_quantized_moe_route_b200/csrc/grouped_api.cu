@@ -36,21 +36,30 @@ int sm_count(int* sms) {
 
 size_t type_bytes(int t) { return t == G_FP32 ? 4 : t == G_E4M3 ? 1 : 2; }
 
+// Rows of `width` bytes, `pitch` bytes apart.
 struct Span {
   const char* name;
   const void* p;
-  size_t bytes;
+  size_t bytes;  // from the first row's first byte to the last row's last
+  size_t pitch, width;
 };
-// `rows` rows of n elements, ld elements apart
-size_t span_bytes(long long rows, long long ld, long long n, int type) {
-  return rows > 0 ? ((size_t)(rows - 1) * ld + n) * type_bytes(type) : 0;
+Span rows_span(const char* name, const void* p, long long rows, long long ld, long long n, int type) {
+  const size_t es = type_bytes(type);
+  return {name, p, rows > 0 ? ((size_t)(rows - 1) * ld + n) * es : 0, (size_t)ld * es, (size_t)n * es};
 }
+Span flat_span(const char* name, const void* p, size_t bytes) { return {name, p, bytes, bytes, bytes}; }
+
 moe_status_t check_apart(const Span& out, const Span* in, int n) {
   const uintptr_t a = (uintptr_t)out.p, b = a + out.bytes;
   for (int i = 0; i < n; ++i) {
     const uintptr_t c = (uintptr_t)in[i].p, d = c + in[i].bytes;
-    if (in[i].p && out.bytes && in[i].bytes && a < d && c < b)
-      return api_fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in[i].name);
+    if (!in[i].p || !out.bytes || !in[i].bytes || b <= c || d <= a) continue;
+    // column ranges of one buffer: the same pitch, and neither row reaches into the other
+    if (out.pitch == in[i].pitch && out.width < out.pitch && in[i].width < out.pitch) {
+      const size_t delta = c >= a ? (c - a) % out.pitch : (out.pitch - (a - c) % out.pitch) % out.pitch;
+      if (delta >= out.width && delta + in[i].width <= out.pitch) continue;
+    }
+    return api_fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out.name, in[i].name);
   }
   return MOE_OK;
 }
@@ -202,12 +211,12 @@ moe_status_t rows_product(const moe_gmm_dims_t* d, const char* in_name, const vo
   const int type = fp8 ? G_E4M3 : d->dtype;
   const long long groups = (d->n_in + 127) / 128;
   const Span ins[5] = {
-      {in_name, in, span_bytes(d->rows, ld_in, in_cols, type)},
-      {"w", w, span_bytes((long long)d->n_experts * d->n_out, d->n_in, d->n_in, type)},
-      {"expert_offsets", off, off ? sizeof(int) * (size_t)(d->n_experts + 1) : 0},
-      {"x_scales", sx, fp8 ? sizeof(float) * (size_t)(groups * d->rows) : 0},
-      {"w_scales", sw, fp8 ? sizeof(float) * (size_t)(groups * d->n_experts * ((d->n_out + 127) / 128)) : 0}};
-  const Span o = {out_name, out, span_bytes(d->rows, ld_out, out_cols, d->out_dtype)};
+      rows_span(in_name, in, d->rows, ld_in, in_cols, type),
+      rows_span("w", w, (long long)d->n_experts * d->n_out, d->n_in, d->n_in, type),
+      flat_span("expert_offsets", off, off ? sizeof(int) * (size_t)(d->n_experts + 1) : 0),
+      flat_span("x_scales", sx, fp8 ? sizeof(float) * (size_t)(groups * d->rows) : 0),
+      flat_span("w_scales", sw, fp8 ? sizeof(float) * (size_t)(groups * d->n_experts * ((d->n_out + 127) / 128)) : 0)};
+  const Span o = rows_span(out_name, out, d->rows, ld_out, out_cols, d->out_dtype);
   GMM_TRY(check_gmm_ws(ws, ws_bytes));
   for (const Span& s : ins)
     if (s.p || s.bytes) GMM_TRY(api_check_dev_ptr(s.p, s.name));
@@ -219,7 +228,7 @@ moe_status_t rows_product(const moe_gmm_dims_t* d, const char* in_name, const vo
   GMM_TRY(check_aligned(ins[4], 4));
   GMM_TRY(check_aligned(o, type_bytes(d->out_dtype)));
   GMM_TRY(check_apart(o, ins, 5));
-  const Span wsp = {"ws", ws, ws_bytes};
+  const Span wsp = flat_span("ws", ws, ws_bytes);
   GMM_TRY(check_apart(o, &wsp, 1));
   GmmProblem p{};
   p.w = w;
@@ -266,10 +275,10 @@ moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64
   const moe_gmm_dims_t& d = *dims;
   GMM_TRY(check_ld(ld_dy, d.n_out, "ld_dy"));
   GMM_TRY(check_ld(ld_x, d.n_in, "ld_x"));
-  const Span ins[3] = {{"dy", dy, span_bytes(d.rows, ld_dy, d.n_out, d.dtype)},
-                       {"x", x, span_bytes(d.rows, ld_x, d.n_in, d.dtype)},
-                       {"expert_offsets", expert_offsets, expert_offsets ? sizeof(int) * (size_t)(d.n_experts + 1) : 0}};
-  const Span o = {"dw", dw, span_bytes((long long)d.n_experts * d.n_out, d.n_in, d.n_in, d.out_dtype)};
+  const Span ins[3] = {
+      rows_span("dy", dy, d.rows, ld_dy, d.n_out, d.dtype), rows_span("x", x, d.rows, ld_x, d.n_in, d.dtype),
+      flat_span("expert_offsets", expert_offsets, expert_offsets ? sizeof(int) * (size_t)(d.n_experts + 1) : 0)};
+  const Span o = rows_span("dw", dw, (long long)d.n_experts * d.n_out, d.n_in, d.n_in, d.out_dtype);
   GMM_TRY(check_gmm_ws(ws, ws_bytes));
   for (const Span& s : ins)
     if (s.bytes) GMM_TRY(api_check_dev_ptr(s.p, s.name));
@@ -279,7 +288,7 @@ moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64
   GMM_TRY(check_aligned(ins[2], 4));
   GMM_TRY(check_aligned(o, type_bytes(d.out_dtype)));
   GMM_TRY(check_apart(o, ins, 3));
-  const Span wsp = {"ws", ws, ws_bytes};
+  const Span wsp = flat_span("ws", ws, ws_bytes);
   GMM_TRY(check_apart(o, &wsp, 1));
   GmmProblem p{};
   p.rows_in = dy;
@@ -313,9 +322,9 @@ moe_status_t moe_quant_fp8(int32_t dtype, int32_t rows, int32_t n_in, const void
   if (rows < 0 || rows > (1 << 30)) return api_fail(MOE_ERR_INVALID_ARG, "rows=%d outside [0, 2^30]", rows);
   GMM_TRY(check_ld(ld_x, n_in, "ld_x"));
   if (rows == 0) return MOE_OK;
-  const Span in = {"x", x, span_bytes(rows, ld_x, n_in, dtype)};
-  const Span o1 = {"codes", codes, (size_t)rows * n_in};
-  const Span o2 = {"scales", scales, (size_t)rows * ((n_in + 127) / 128) * 4};
+  const Span in = rows_span("x", x, rows, ld_x, n_in, dtype);
+  const Span o1 = flat_span("codes", codes, (size_t)rows * n_in);
+  const Span o2 = flat_span("scales", scales, (size_t)rows * ((n_in + 127) / 128) * 4);
   GMM_TRY(api_check_dev_ptr(x, "x"));
   GMM_TRY(api_check_dev_ptr(codes, "codes"));
   GMM_TRY(api_check_dev_ptr(scales, "scales"));

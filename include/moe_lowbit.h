@@ -372,11 +372,12 @@ size_t moe_grouped_workspace_size(void);
  *        MOE_ERR_DEVICE_INPUT and nothing is written.  NULL with n_experts =
  *        1: one matrix for every row.
  *   y  : [rows, n_out] (out), ld_y >= n_out; overlaps no input
- * Pointers are aligned to their elements.  Operands whose base address and
- * row stride (and, for the weights, row length) are multiples of 16 bytes run
- * on the tcgen05 kernel, others on a slower one with the same results up to
- * the order of the fp32 sums.  Results do not depend on what else runs: the
- * same call gives the same bits.
+ *        (column ranges of one buffer with one row stride may lie side by side)
+ * Pointers are aligned to their elements.  Operands whose base address, row
+ * stride and (weights) row length are multiples of 16 bytes are copied by TMA;
+ * others come through registers, more slowly (about a fifth of the rate of
+ * large products), with the same results up to the order of the fp32 sums.
+ * Results do not depend on what else runs: the same call gives the same bits.
  */
 moe_status_t moe_grouped_mm(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const void* w,
                             const int32_t* expert_offsets, void* y, int64_t ld_y, void* ws, size_t ws_bytes,

@@ -269,6 +269,72 @@ def test_overlap_and_host_memory_refused(cuda_device, ws):
         moe.quant_fp8(x, x.view(-1).view(torch.uint8)[:512].view(8, 64), s)
 
 
+def test_column_ranges_of_one_buffer(cuda_device, ws):
+    """Input and output side by side in one buffer are apart; ranges that share a column are not."""
+    g = gen(12, cuda_device)
+    buf = normal(g, BF, 40, 320)
+    w = normal(g, BF, 1, 128, 192, std=0.1)
+    x, y = buf[:, :192], buf[:, 192:]
+    ref, mag = reference("mm", x, w, None, 1)
+    keep = x.clone()
+    moe.grouped_mm(x, w, None, y, ws)
+    close(y, ref, mag, 192)
+    assert torch.equal(x, keep)
+    dx = buf[:, 128:]
+    moe.grouped_mm_dx(buf[:, :128], w, None, dx, ws)             # the other order
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.grouped_mm(buf[:, :192], w, None, buf[:, 191:319], ws)
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.grouped_mm(buf[:, 100:292], w, None, buf[:, :128], ws)
+
+
+def test_range_of_fp16(cuda_device, ws):
+    """Sums beyond fp16 become infinite; subnormal operands count."""
+    for n_in in (64, 63):
+        x, w = torch.full((4, n_in), 300.0, dtype=HF, device=cuda_device), torch.zeros(1, 16, n_in, dtype=HF, device=cuda_device)
+        w[0, 0], w[0, 1] = 300.0, -300.0
+        w[0, 2, 0] = 2.0 ** -24                                    # the smallest fp16 subnormal
+        y = torch.zeros(4, 16, dtype=HF, device=cuda_device)
+        moe.grouped_mm(x, w, None, y, ws)
+        assert bool((y[:, 0] == float("inf")).all()) and bool((y[:, 1] == float("-inf")).all())
+        assert bool((y[:, 2] == torch.tensor(300 * 2.0 ** -24, dtype=HF, device=cuda_device)).all())
+        assert bool((y[:, 3:] == 0).all())
+
+
+FIRST_CALL = """
+import torch, bit_quantized_moe_route_b200 as moe
+dev = torch.device("cuda:0")
+ws = moe.alloc_grouped_workspace(dev)
+off = torch.tensor([0, 3, 3, 10], dtype=torch.int32, device=dev)
+side = torch.cuda.Stream(dev)
+for n_in in (128, 127):
+    x = torch.ones(10, n_in, dtype=torch.bfloat16, device=dev)
+    w = torch.ones(3, 64, n_in, dtype=torch.bfloat16, device=dev)
+    y, dx = torch.zeros(10, 64, device=dev), torch.zeros(10, n_in, device=dev)
+    dw = torch.full((3, 64, n_in), 5.0, device=dev)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):      # the process's first calls
+        moe.grouped_mm(x, w, off, y, ws)
+        moe.grouped_mm_dx(x.new_ones(10, 64), w, off, dx, ws)
+        moe.grouped_mm_dw(x.new_ones(10, 64), x, off, dw, ws)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert bool((y == n_in).all()) and bool((dx == 64).all())
+    assert dw[0].unique().tolist() == [3.0] and dw[1].unique().tolist() == [0.0] and dw[2].unique().tolist() == [7.0]
+assert moe.read_device_error(ws) == 0
+print("ok")
+"""
+
+
+def test_first_call_in_a_capture(cuda_device):
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
 def test_streams_and_graphs(cuda_device):
     """Two streams with a workspace each, and a captured call replayed on new inputs."""
     g = gen(8, cuda_device)
