@@ -321,6 +321,7 @@ struct alignas(16) GuLine {
   int off[kGmmMaxExperts + 1];      // the experts' rows
   int cum[kGmmMaxExperts + 1];      // the experts' tiles
   int chunk[kGmmMaxExperts / 32];
+  int steps_most;                   // dw: of a tile
 };
 
 // shared memory from the first 1024-byte boundary: operand ring, scales, the
@@ -335,6 +336,7 @@ static_assert(gu_smem() <= 227 * 1024, "shared memory");
 template <int OP, bool FP8, bool ROWM, int MT_>
 struct GuTiles {
   static constexpr int MT = MT_;
+  static constexpr bool kRowsM = ROWM, kFp8 = FP8;
   static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
   static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
   // N values per MMA in multiples of 16 (8-bit: 32; dw: whole 64-value panels in both CTAs)
@@ -489,6 +491,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   };
 #pragma unroll 4
   for (int e = tid; e <= p.E; e += NT) l.off[e] = gmm_off(p, e);
+  if (tid == 0) l.steps_most = 0;
   sync();
   int bad = 0;
   const int chunks = (p.E + 31) >> 5;
@@ -499,6 +502,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       const int a = l.off[e], b = l.off[e + 1];
       if (a < 0 || b < a || b > p.rows) bad = 1;
       else n = Tiles::of_expert(p, b - a);
+      if (OP == G_DW && !bad) atomicMax(&l.steps_most, Tiles::steps(p, b - a));
     }
     int x = n;
 #pragma unroll
@@ -545,20 +549,44 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       atomicAdd(reinterpret_cast<unsigned long long*>(&l.hand[q]), (unsigned long long)c);
     }
   }
-  // What is left (halves of tiles for MT = 2; at most kGuTailMost - 1).  mm, dx,
-  // all of one length: as many as there are for every pair are dealt too, and
-  // each of the others is cut evenly for as many pairs as there are, unless
-  // the line is shorter in all (its sums to join cost as much as some 24
-  // steps, and pairs have two of them).
+  // What is left (halves of tiles for MT = 2; at most kGuTailMost - 1): as many
+  // as there are for every pair are dealt too, and each of the others is cut
+  // evenly, for at most as many pairs as there are, or all of it is the line,
+  // whichever costs less.  Measured, in us, for tiles of np columns: a step
+  // 0.145 + np / 3000 (8-bit of over 64 columns, which hand over every other
+  // step: 0.45); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
+  // steps of 32 columns: whole 33.0, in four 18.2, eight 17.2, sixteen 20.1; 19
+  // steps of 240: whole 13.6, in two 20.7.  dw, whose tiles differ in length:
+  // dealt if the longest are short, else the line.
   int halves = 0, each_in = 0;
-  if constexpr (OP != G_DW) {
-    const int steps = Tiles::steps(p, 0), q = rest / cols, r = rest - q * cols;
-    const int k = r ? min(split_most, cols / r) : 1;
-    const float even = q * steps + (r ? (float)steps / k : 0.f) + (k > 1 ? 24.f : 0.f);
-    const float line = (float)steps * rest / cols + 36.f;
-    if (even <= line) {
-      halves = q;
-      each_in = k;
+  {
+    const int q = rest / cols, r = rest - q * cols;
+    if constexpr (OP == G_DW) {
+      if (l.steps_most <= 40) {
+        halves = q;
+        each_in = 1;
+      }
+    } else {
+      const float steps = (float)Tiles::steps(p, 0);
+      const int rows = l.off[p.E] - l.off[0], m_tiles = max(1, Tiles::m_count(p, rows));
+      // columns of a tile, on average
+      const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out) : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
+      const float step = Tiles::kFp8 && np > 64.f ? 0.45f : 0.145f + np * (1.f / 3000.f);
+      const float join = 0.4f + np * (1.f / 62.f), part = 0.2f + np * (1.f / 154.f);
+      float best = r ? steps * step : 0.f;
+      int k = 1;
+      for (int i = 2; r && i <= min(split_most, cols / r); ++i) {
+        const float c = steps * step / i + join + i * part;
+        if (c < best) {
+          best = c;
+          k = i;
+        }
+      }
+      const float line = steps * step * rest / cols + 1.5f * (join + 2.5f * part);
+      if (q * steps * step + best <= line) {
+        halves = q;
+        each_in = k;
+      }
     }
   }
   const int tails = rest - halves * cols;
@@ -683,63 +711,7 @@ MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int 
   __syncwarp();
 }
 
-// 32 bytes to a 32-byte aligned address: one whole sector per lane and store
-// (with 16 the lanes of a warp, each in a row of its own, fill half sectors)
-MOE_DEV void gu_st256(void* p, uint4 a, uint4 b) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
-               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-MOE_DEV uint4 gu_bits4(const float* v) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-}
-// Rows on the M side: W values of this lane's row, from element `base` on, of
-// which `left` are there; `unit`: the rows' alignment, 32, 16 or less.  F32:
-// what is known of the type (1: fp32, 0: 16 bits, -1: nothing).
-template <int W, int F32>
-MOE_DEV void gu_row_out(void* out, int type, long long base, int left, int unit, const float* v) {
-  const bool f32 = F32 < 0 ? type == G_FP32 : F32 == 1;
-  if (unit >= 16 && left >= W) {
-    char* o = reinterpret_cast<char*>(out) + base * (f32 ? 4 : 2);
-    if (f32) {
-#pragma unroll
-      for (int i = 0; i < W; i += 8) {
-        if (unit == 32) {
-          gu_st256(o + 4 * i, gu_bits4(v + i), gu_bits4(v + i + 4));
-        } else {
-          *reinterpret_cast<uint4*>(o + 4 * i) = gu_bits4(v + i);
-          *reinterpret_cast<uint4*>(o + 4 * i + 16) = gu_bits4(v + i + 4);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; i += 16) {
-        const uint4 a = gu_pack8(type, v + i), b = gu_pack8(type, v + i + 8);
-        if (unit == 32) {
-          gu_st256(o + 2 * i, a, b);
-        } else {
-          *reinterpret_cast<uint4*>(o + 2 * i) = a;
-          *reinterpret_cast<uint4*>(o + 2 * i + 16) = b;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (i < left) {
-        if (f32) {
-          reinterpret_cast<float*>(out)[base + i] = v[i];
-        } else {
-          const uint16_t b = type == G_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[i]))
-                                            : __half_as_ushort(__float2half_rn(v[i]));
-          reinterpret_cast<uint16_t*>(out)[base + i] = b;
-        }
-      }
-  }
-}
-
-// The same two for 16 values that are rounded already: rows on the N side as
-// 16-bit words [row][lane] in `buf`; rows on the M side, pairs of this lane's row.
+// The same for values that are rounded already, as 16-bit words [row][lane] in `buf`.
 MOE_DEV void gu_rows_out16(void* out, long long base, long long ld, int rows, int vals, bool vec, uint32_t buf) {
   const int lane = threadIdx.x & 31;
   uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
@@ -755,21 +727,71 @@ MOE_DEV void gu_rows_out16(void* out, long long base, long long ld, int rows, in
   }
   __syncwarp();
 }
-MOE_DEV void gu_row_out16(void* out, long long base, int left, int unit, const uint32_t* w) {
-  uint16_t* o = reinterpret_cast<uint16_t*>(out) + base;
-  if (unit >= 16 && left >= 16) {
-    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
-    if (unit == 32) {
-      gu_st256(o, a, b);
-    } else {
-      *reinterpret_cast<uint4*>(o) = a;
-      *reinterpret_cast<uint4*>(o + 8) = b;
-    }
-  } else {
+// Rows on the M side: LB bytes (64 or 128) of each lane's row leave through
+// shared memory, 2 KB at a time, so that every store is of that many
+// neighbouring bytes (with each lane storing to its own row in 32-byte sectors,
+// weights' gradients of few rows, which are all stores, ran at 1.4 TB/s).  w:
+// the lane's values, from element `base` of the warp's first row on, `left` of
+// them in `vals` rows.
+template <bool F32, int LB>
+MOE_DEV void gu_lines_out(void* out, long long base, long long ld, int left, int vals, int unit, const uint32_t* w,
+                          uint32_t buf) {
+  constexpr int ES = F32 ? 4 : 2, PER = 16 / ES, CH = LB / 16, ROWS = 2048 / LB;
+  const int lane = threadIdx.x & 31;
+  char* o = reinterpret_cast<char*>(out) + base * ES;
+  auto place = [&](int r, int c) {
+    return buf + (uint32_t)(r * LB + ((CH == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+  };
+  auto value = [&](char* to, uint32_t from) {
+    if (F32) *reinterpret_cast<uint32_t*>(to) = tc_lds32(from);
+    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)um_lds16(from);
+  };
+  // (rolled loops: this is expanded at several places, and the 8-bit products
+  // took 358 us instead of 333 with code that the instruction caches do not hold)
+#pragma unroll 1
+  for (int r0 = 0; r0 < vals; r0 += ROWS) {
+    const int rows = min(ROWS, vals - r0);
+    __syncwarp();
+    if (ROWS == 32 || lane / ROWS == r0 / ROWS) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      for (int c = 0; c < CH; ++c) tc_sts128(place(lane % ROWS, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    }
+    __syncwarp();
+    const int c = lane % CH;
+    char* to = o + ((long long)(r0 + lane / CH) * ld + PER * c) * ES;
+    if (unit >= 16 && left >= PER * CH) {
+#pragma unroll
+      for (int i = 0; i < ROWS; i += 32 / CH) {
+        if (i + lane / CH < rows) *reinterpret_cast<uint4*>(to) = tc_lds128(place(i + lane / CH, c));
+        to += (long long)(32 / CH) * ld * ES;
+      }
+    } else if (unit >= 16) {
+      const int n = min(PER, left - PER * c);  // valid values of this lane's 16 bytes
+#pragma unroll 1
+      for (int r = lane / CH; r < rows; r += 32 / CH, to += (long long)(32 / CH) * ld * ES) {
+        const uint32_t from = place(r, c);
+        if (n == PER) *reinterpret_cast<uint4*>(to) = tc_lds128(from);
+        else
+#pragma unroll 1
+          for (int k = 0; k < n; ++k) value(to + k * ES, from + k * ES);
+      }
+    } else {  // rows at any element: 32 neighbouring values per store
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r)
+#pragma unroll 1
+        for (int v = lane; v < min(left, LB / ES); v += 32)
+          value(o + ((r0 + r) * ld + v) * ES, place(r, v * ES >> 4) + (uint32_t)(v * ES & 15));
+    }
   }
+  __syncwarp();
+}
+
+// 32 bytes to a 32-byte aligned address: one whole sector per lane and store
+// (with 16 the lanes of a warp, each in a row of its own, fill half sectors)
+MOE_DEV void gu_st256(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // ------------------------------------------------------------ the kernel
@@ -1296,30 +1318,48 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
       GuItem it;
       if (!copy_item(it, false)) break;
       const int chunks = (it.np + 31) >> 5;
+      // This warp's 32-column ranges: every H-th, or (rows on the M side, for
+      // longer stores) neighbours; 8-bit: those of one scale block.
+      const int share = FP8 ? 4 : (chunks + 1) >> 1;
+      const int c_first = ROWM ? h * share : h, c_end = ROWM && h == 0 ? min(share, chunks) : chunks;
+      constexpr int C_STEP = ROWM ? 1 : H;
       const bool all = it.kb0 == 0 && it.kb1 == it.nkb;
       const int m = (int)rank * 128 + 32 * q;       // the warp's first M value in the tile
       int vals = min(32, it.mv - m);                // how many it has
-      // the first M and N value's output element (rows on the M side: this lane's row)
-      long long ob =
-          ROWM ? (OP == G_DW ? (long long)it.e * g.n_out + it.m0 + m + lane : (long long)it.m0 + m + lane) * ld + it.n0
-               : (long long)it.n0 * ld + it.m0 + m;
-      // N values SR c .. of the tile, from v[at] on
-      auto out_sr = [&](int c, const auto& v, const int at) {
-        const int left = it.nv - SR * c;
+      // the first M and N value's output element
+      long long ob = ROWM ? (OP == G_DW ? (long long)it.e * g.n_out + it.m0 + m : (long long)it.m0 + m) * ld + it.n0
+                          : (long long)it.n0 * ld + it.m0 + m;
+      // N values 32 c .. of the tile to the output
+      auto out32 = [&](int c, const float (&v)[32]) {
+        const int left = it.nv - 32 * c;
         if (left <= 0 || vals <= 0) return;
         if constexpr (ROWM) {
-          if (lane < vals) gu_row_out<SR, F32>(g.out, g.out_type, ob + SR * c, left, unit, &v[at]);
+          const bool f32 = F32 < 0 ? g.out_type == G_FP32 : F32 == 1;
+          uint32_t w[32];
+          if (f32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+            if constexpr (F32 != 0) gu_lines_out<true, 128>(g.out, ob + 32 * c, ld, left, vals, unit, w, buf);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+            if constexpr (F32 != 1) gu_lines_out<false, 64>(g.out, ob + 32 * c, ld, left, vals, unit, w, buf);
+          }
         } else {
 #pragma unroll
-          for (int i = 0; i < SR; ++i)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[at + i]) : "memory");
-          gu_rows_out<F32>(g.out, g.out_type, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
+          for (int u = 0; u < 32; u += SR)
+            if (left > u) {
+#pragma unroll
+              for (int i = 0; i < SR; ++i)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (uint32_t)(i * 128 + 4 * lane)), "f"(v[u + i]) : "memory");
+              gu_rows_out<F32>(g.out, g.out_type, ob + (32 * c + u) * ld, ld, min(SR, left - u), vals,
+                               unit >= 16 && vals == 32, buf);
+            }
         }
       };
-      auto put = [&](int c, const float (&v)[32]) {  // N values 32 c ..
+      auto put = [&](int c, const float (&v)[32]) {  // ... or to this pair's part
         if (all) {
-          out_sr(2 * c, v, 0);
-          out_sr(2 * c + 1, v, 16);
+          out32(c, v);
         } else {
           float4* part = part_of((int)pair, it.kb0 > 0 ? 0 : 1) + 8 * c * 128;
 #pragma unroll
@@ -1327,12 +1367,24 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             __stcg(part + i * 128, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
         }
       };
+      // 64 rounded values from 32 c on (rows on the M side)
+      auto out64 = [&](int c, const uint32_t* w) {
+        const int left = it.nv - 32 * c;
+        if (left > 0 && vals > 0) gu_lines_out<false, 128>(g.out, ob + 32 * c, ld, left, vals, unit, w, buf);
+      };
       if (it.kind == GU_ZEROS) {
-        float z[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0.f;
         for (int half = 0; half < it.halves; ++half) {
-          for (int c = h; c < chunks; c += H) put(c, z);
+          if constexpr (F32 == 0 && ROWM) {
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0;
+            for (int c = c_first; c < c_end; c += 2) out64(c, z);
+          } else {
+            float z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0.f;
+            for (int c = c_first; c < c_end; c += C_STEP) out32(c, z);
+          }
           ob += ROWM ? 256 * ld : 256;
           vals = min(32, it.mv - 256 - m);
         }
@@ -1355,21 +1407,24 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
           // halves, so that the accumulators are free before the first store:
           // the next tile's MMAs wait for 800 clocks of TMEM reads then, and
           // not for 4,800 more of stores.
-          uint32_t w[MT][4][16];
+          uint32_t w[MT][64];
 #pragma unroll
           for (int half = 0; half < MT; ++half)
             if (half < it.halves) {
               const int at = ring.take(it.np);
               ok = ok && wait_sums();
               if (ok) {
-                const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+                const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  if (H * j + h < chunks) {
+                  if (c_first + C_STEP * j < c_end) {
                     float v[32];
-                    gu_ld32(ta + 64u * j, v);
+                    gu_ld32(ta + 32u * (c_first + C_STEP * j), v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[half][j][i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 16; ++i) w[half][16 * j + i] = gu_pack2(g.out_type, v[2 * i], v[2 * i + 1]);
+                  } else if (ROWM && (j & 1)) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[half][16 * j + i] = 0;
                   }
                 give_back();
                 ++seg;
@@ -1379,26 +1434,33 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
 #pragma unroll
           for (int half = 0; half < MT; ++half) {
             if (half >= it.halves) break;
+            if constexpr (ROWM) {
+              // 64 values where this warp has both ranges; a last one alone ends before its neighbour's
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (H * j + h < chunks) {
+              for (int j = 0; j < 4; j += 2) {
+                const int c = c_first + j;
+                if (c + 1 < c_end) out64(c, &w[half][16 * j]);
+                else if (c < c_end && it.nv > 32 * c && vals > 0)
+                  gu_lines_out<false, 64>(g.out, ob + 32 * c, ld, it.nv - 32 * c, vals, unit, &w[half][16 * j], buf);
+              }
+            } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const int c = 2 * (H * j + h) + u, left = it.nv - SR * c;
-                  if (left <= 0 || vals <= 0) continue;
-                  if constexpr (ROWM) {
-                    if (lane < vals) gu_row_out16(g.out, ob + SR * c, left, unit, &w[half][j][8 * u]);
-                  } else {
+              for (int j = 0; j < 4; ++j)
+                if (H * j + h < chunks) {
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    const int c = 2 * (H * j + h) + u, left = it.nv - SR * c;
+                    if (left <= 0 || vals <= 0) continue;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                      const uint32_t to = buf + (uint32_t)(128 * i + 2 * lane), x = w[half][j][8 * u + i];
+                      const uint32_t to = buf + (uint32_t)(128 * i + 2 * lane), x = w[half][16 * j + 8 * u + i];
                       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"((uint16_t)x) : "memory");
                       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64), "h"((uint16_t)(x >> 16)) : "memory");
                     }
                     gu_rows_out16(g.out, ob + SR * c * ld, ld, min(SR, left), vals, unit >= 16 && vals == 32, buf);
                   }
                 }
-              }
+            }
             ob += ROWM ? 256 * ld : 256;  // the second half's M values
             vals = min(32, it.mv - 256 - m);
           }
@@ -1406,7 +1468,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
           const int at = ring.take(it.np);
           ok = wait_sums();
           if (!ok) break;
-          for (int c = h; c < chunks; c += H) {
+          for (int c = c_first; c < c_end; c += C_STEP) {
             float v[32];
             gu_ld32(lane_addr + (uint32_t)(at * kGuSlotCols + 32 * c), v);
             put(c, v);
@@ -1449,46 +1511,43 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             ++seg;
           }
         } else if constexpr (FP8) {
-          // one row scale per thread and step, one weight scale per half of
-          // the columns; those of the next steps are on their way
+          // one row scale per thread and step, and one weight scale per warp
+          // (128 columns); those of the next steps are on their way
           const int groups = (g.n_in + 127) >> 7, blocks = (g.n_out + 127) >> 7;
           const float* sxp = g.sx + it.m0 + m + min(lane, max(vals - 1, 0));
-          const float* swp = g.sw + ((long long)it.e * blocks + (it.n0 >> 7)) * groups;
-          const int second = (it.n0 >> 7) + 1 < blocks ? groups : 0;
-          auto scale_of = [&](int kb, float& x, float& a, float& b) {
+          const float* swp = g.sw + ((long long)it.e * blocks + min((it.n0 >> 7) + h, blocks - 1)) * groups;
+          auto scale_of = [&](int kb, float& x, float& a) {
             kb = min(kb, it.kb1 - 1);
             x = vals > 0 ? __ldg(sxp + (long long)kb * g.rows) : 0.f;
             a = __ldg(swp + kb);
-            b = __ldg(swp + second + kb);
           };
-          float x0, a0, b0, x1, a1, b1;
-          scale_of(it.kb0, x0, a0, b0);
-          scale_of(it.kb0 + 1, x1, a1, b1);
+          float x0, a0, x1, a1;
+          scale_of(it.kb0, x0, a0);
+          scale_of(it.kb0 + 1, x1, a1);
           for (int kb = it.kb0; kb < it.kb1; ++kb) {
             const int at = ring.take(kGuN);
-            const float sa = x0 * a0, sb = x0 * b0;
-            const unsigned long long s0 = gu_pack(sa, sa), s1 = gu_pack(sb, sb);
-            x0 = x1, a0 = a1, b0 = b1;
-            scale_of(kb + 2, x1, a1, b1);
+            const float sa = x0 * a0;
+            const unsigned long long sc = gu_pack(sa, sa);
+            x0 = x1, a0 = a1;
+            scale_of(kb + 2, x1, a1);
             ok = wait_sums();
             if (!ok) break;
-            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
-            // columns 64 j + 32 h, j = 0..3 (those beyond the tile's hold what
-            // was there before and are not stored)
+            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 128 * h);
+            // (columns beyond the tile's hold what was there before and are not stored)
             uint32_t r0[32], r1[32];
             gu_ld_issue(ta, r0);
             gu_ld_wait(r0);
-            gu_ld_issue(ta + 64, r1);
-            gu_times(acc[0], r0, s0);
+            gu_ld_issue(ta + 32, r1);
+            gu_times(acc[0], r0, sc);
             gu_ld_wait(r1);
-            gu_ld_issue(ta + 128, r0);
-            gu_times(acc[1], r1, s0);
+            gu_ld_issue(ta + 64, r0);
+            gu_times(acc[1], r1, sc);
             gu_ld_wait(r0);
-            gu_ld_issue(ta + 192, r1);
-            gu_times(acc[2], r0, s1);
+            gu_ld_issue(ta + 96, r1);
+            gu_times(acc[2], r0, sc);
             gu_ld_wait(r1);
             give_back();
-            gu_times(acc[3], r1, s1);
+            gu_times(acc[3], r1, sc);
             ++seg;
           }
         } else {
@@ -1496,12 +1555,12 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             const int at = ring.take(it.np);
             ok = wait_sums();
             if (!ok) break;
-            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols + 32 * h);
+            const uint32_t ta = lane_addr + (uint32_t)(at * kGuSlotCols);
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-              if (H * j + h < chunks) {
+              if (c_first + C_STEP * j < c_end) {
                 uint32_t r[32];
-                gu_ld_issue(ta + 64u * j, r);
+                gu_ld_issue(ta + 32u * (c_first + C_STEP * j), r);
                 gu_ld_wait(r);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2)
@@ -1512,14 +1571,40 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
           }
         }
         if (!ok) break;
+        if (FP8 && ROWM && all && g.out_type != G_FP32) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (H * j + h < chunks) {
-            float v[32];
+          for (int j = 0; j + 1 < NJ; j += 2) {
+            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) gu_unpack(acc[j][i], v[2 * i], v[2 * i + 1]);
-            put(H * j + h, v);
+            for (int i = 0; i < 32; ++i) {
+              float lo, hi;
+              gu_unpack(acc[j + i / 16][i % 16], lo, hi);
+              w[i] = gu_pack2(g.out_type, lo, hi);
+            }
+            const int c = c_first + j, left = it.nv - 32 * c;
+            if (left <= 0 || vals <= 0) continue;
+            if (left >= 64 && unit == 32) {
+              // (straight from the registers: the next sums cannot be taken
+              // from tensor memory meanwhile, and this is the shorter way)
+              uint16_t* o = reinterpret_cast<uint16_t*>(g.out) + ob + lane * ld + 32 * c;
+              if (lane < vals) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) gu_st256(o + 2 * i, w + i);
+              }
+            } else {
+              out64(c, w);
+            }
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            if (c_first + C_STEP * j < c_end) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) gu_unpack(acc[j][i], v[2 * i], v[2 * i + 1]);
+              put(c_first + C_STEP * j, v);
+            }
+        }
       }
       if (!all) {
         // Count this part in; the last part's CTA adds them all, in the
@@ -1561,7 +1646,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
           __threadfence();
           // 32 columns at a time, two parts' loads in flight together
 #pragma unroll 1
-          for (int c = h; c < chunks; c += H) {
+          for (int c = c_first; c < c_end; c += C_STEP) {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -1590,8 +1675,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
                   }
               }
             }
-            out_sr(2 * c, v, 0);
-            out_sr(2 * c + 1, v, 16);
+            out32(c, v);
           }
         }
       }
