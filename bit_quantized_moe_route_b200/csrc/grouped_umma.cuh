@@ -35,11 +35,11 @@
 // value of another expert's rows (a NaN, say) enters a product.
 //
 // LDG: operands of any alignment and row stride, which TMA cannot read.  Eight
-// more warps bring each step in: a 16-byte piece at any address is cut out of
-// the two aligned 16-byte blocks that hold it (both inside the operand, else
-// byte by byte) and stored where TMA would have put it; values beyond the
-// matrix or the expert's rows are zeros.  Bound by those loads' latency and
-// the instructions around them.
+// more warps copy the 16-byte aligned blocks that hold each step's rows to
+// shared memory, three steps at a time on their way (asynchronous copies: no
+// register waits; zeros beyond the matrix or the expert's rows), cut the
+// operands' 16-byte pieces out of two neighbouring blocks each and store them
+// where TMA would have put them.
 //
 // The tiles, in the order expert, M tile, row tile, are dealt out to the pairs
 // of CTAs in turn, so that pairs that run at the same time read the same
@@ -77,6 +77,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "ffn_umma.cuh"
 #include "grouped_plan.cuh"
 
@@ -84,6 +86,10 @@ namespace moe {
 
 constexpr int kGuTile = 16384;            // bytes of 128 operand rows of one step
 constexpr int kGuRing = 12 * kGuTile;
+// LDG: two stages, and the aligned blocks of three steps
+constexpr int kGuRaw = 128 * (128 + 16);  // (64 rows of 256 + 16 are less)
+constexpr int kGuRaws = 3;
+static_assert(2 * 2 * kGuTile + kGuRaws * 2 * kGuRaw <= kGuRing, "operand ring");
 constexpr int kGuN = 256;                 // output rows per tile
 // Warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 the epilogue, two for each 32
 // TMEM lanes.  (Sixteen epilogue warps were slower: each barrier wait and
@@ -98,8 +104,8 @@ constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
 // LDG: eight more warps; less for each.
 constexpr int kGuLoadWarps = 8;
 constexpr int gu_threads(bool ldg) { return kGuThreads + (ldg ? 32 * kGuLoadWarps : 0); }
-constexpr int kGuLdgRegs = 96, kGuLdgLow = 64, kGuLdgHigh = 112;  // (the load warps keep theirs)
-static_assert(128 * kGuLdgLow + 32 * kGuLoadWarps * kGuLdgRegs + 32 * kGuEpiWarps * kGuLdgHigh <= gu_threads(true) * kGuLdgRegs,
+constexpr int kGuLdgRegs = 96, kGuLdgLow = 64, kGuLdgLoad = 80, kGuLdgHigh = 128;
+static_assert(128 * kGuLdgLow + 32 * kGuLoadWarps * kGuLdgLoad + 32 * kGuEpiWarps * kGuLdgHigh <= gu_threads(true) * kGuLdgRegs,
               "registers of the block");
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
@@ -244,54 +250,40 @@ MOE_DEV void gu_times(unsigned long long (&acc)[16], const uint32_t (&r)[32], un
   for (int i = 0; i < 32; i += 2) gu_fma2(acc[i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
 }
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
-// LDG: a 16-byte piece on its way, n valid bytes from p on, of an operand
-// whose bytes are [lo, hi).
-struct GuPiece {
-  uint4 a, b;
-  MOE_DEV void load(const char* p, int n, const char* lo, const char* hi) {
-    if (n <= 0) return;
-    const char* p0 = p - (reinterpret_cast<uintptr_t>(p) & 15);
-    if (p0 >= lo && p0 + 32 <= hi) {
-      a = __ldg(reinterpret_cast<const uint4*>(p0));
-      b = __ldg(reinterpret_cast<const uint4*>(p0) + 1);
-    } else {  // at an end of the operand
-      unsigned long long w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[k] = 0;
+// LDG: 16 bytes from `from` (16-byte aligned) to shared memory, on their way
+MOE_DEV void gu_fetch16(uint32_t to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// ... where those from `end` on are zeros and, like those before `lo` (the
+// operand's first byte), not read.
+MOE_DEV void gu_fetch16(uint32_t to, const char* from, const char* end, const char* lo) {
+  const long long left = end - from;
+  const uint32_t n = left >= 16 ? 16u : left > 0 ? (uint32_t)left : 0u;
+  if (from < lo && n > 0) {
 #pragma unroll 1
-        for (int i = 7; i >= 0; --i) {
-          const char* q = p0 + 8 * k + i;
-          w[k] = w[k] << 8 | (q >= lo && q < hi ? *reinterpret_cast<const uint8_t*>(q) : 0u);
-        }
-      }
-      a = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
-      b = make_uint4((uint32_t)w[2], (uint32_t)(w[2] >> 32), (uint32_t)w[3], (uint32_t)(w[3] >> 32));
+    for (int i = 0; i < 16; ++i) {
+      const char* q = from + i;
+      const uint16_t x = q >= lo && q < end ? *reinterpret_cast<const uint8_t*>(q) : 0;
+      asm volatile("{ .reg .b8 t; cvt.u8.u16 t, %1; st.shared.b8 [%0], t; }" ::"r"(to + i), "h"(x) : "memory");
     }
+  } else {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(n > 0 ? from : lo - (reinterpret_cast<uintptr_t>(lo) & 15)),
+                 "r"(n)
+                 : "memory");
   }
-  // shift: p's last four bits
-  MOE_DEV void store(uint32_t to, int n, uint32_t shift) const {
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (n > 0) {
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t t[6], u[5];
+}
+// the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
+MOE_DEV void gu_cut16(uint32_t to, uint4 a, uint4 b, uint32_t shift) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t t[6], u[5], o[4];
 #pragma unroll
-      for (int i = 0; i < 6; ++i) t[i] = shift & 8 ? w[i + 2] : w[i];
+  for (int i = 0; i < 6; ++i) t[i] = shift & 8 ? w[i + 2] : w[i];
 #pragma unroll
-      for (int i = 0; i < 5; ++i) u[i] = shift & 4 ? t[i + 1] : t[i];
+  for (int i = 0; i < 5; ++i) u[i] = shift & 4 ? t[i + 1] : t[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], (shift & 3) * 8);
-      if (n < 16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int left = n - 4 * i;  // valid bytes of this word
-          o[i] = left >= 4 ? o[i] : left <= 0 ? 0u : o[i] & (0xFFFFFFFFu >> (32 - 8 * left));
-        }
-      }
-    }
-    tc_sts128(to, o[0], o[1], o[2], o[3]);
-  }
-};
+  for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], (shift & 3) * 8);
+  tc_sts128(to, o[0], o[1], o[2], o[3]);
+}
 
 // ------------------------------------------------------------ work items
 // A run of steps of one tile.
@@ -804,7 +796,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
   static_assert(MT == 1 || (CHAIN == 0 && !LDG), "register sums and loads hold one MMA's");
   // what the kernel knows of the output's type: 1 fp32, 0 16 bits, -1 nothing
   constexpr int F32 = FP8 || LDG ? -1 : CHAIN ? 1 : 0;
-  constexpr int NS = 12 / (MT + 1);           // stages
+  constexpr int NS = LDG ? 2 : 12 / (MT + 1);  // stages
   constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
   using Tiles = GuTiles<OP, FP8, ROWM, MT>;
   using Walk = GuWalk<Tiles>;
@@ -1202,89 +1194,154 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
     }
   } else if (LDG && warp >= 4 + kGuEpiWarps) {
     if constexpr (LDG) {
-      // ================= loads of any alignment: A and B of each step, four
-      // pieces of each per thread
+      // ================= loads of any alignment: the aligned blocks that hold
+      // a step's rows, kGuRaws - 1 steps ahead of the cutting: for each of the
+      // 128 rows of a K-major operand nine blocks for 128 bytes, for each of
+      // the 64 contracted rows of an M- or N-major one 17 for 256 bytes of
+      // values (two panels).  A warp cuts the rows that it has loaded itself.
+      // (What precedes a row's first byte in its block is the same for all
+      // steps of an item: they are multiples of 16 bytes apart.)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLoad));
       constexpr int ES = FP8 ? 1 : 2;
-      const int lt = tid - kGuThreads;  // 0 .. 255
+      const int lw = warp - 4 - kGuEpiWarps;  // 0 .. 7
       const char* w_lo = reinterpret_cast<const char*>(g.w);
-      const char* w_hi = w_lo + (long long)g.E * g.n_out * g.n_in * ES;
       const char* r_lo = reinterpret_cast<const char*>(g.rows_in);
-      const char* r_hi = r_lo + ((long long)(g.rows - 1) * g.ld_rows + (OP == G_MM ? g.n_in : g.n_out)) * ES;
       const char* x_lo = reinterpret_cast<const char*>(g.x);
-      const char* x_hi = x_lo + ((long long)(g.rows - 1) * g.ld_x + g.n_in) * ES;
-      // K-major: row (lt >> 3) + 32 j, 16-byte piece lt & 7 of the step's 128
-      // bytes; `rows` there are, `len` bytes left of each
-      auto k_major = [&](uint32_t dst, const char* p, long long ld, int rows, int len, const char* lo, const char* hi) {
-        const int c = lt & 7, r0 = lt >> 3;
-        GuPiece v[4];
+      const long long ldw = (long long)g.n_in * ES, ldr = g.ld_rows * ES, ldx = g.ld_x * ES;
+      const uint32_t raw0 = base + NS * kStep;
+      auto fetch = [&](auto mn, uint32_t to, const char* q, long long ld, int rows, int len, const char* lo) {
+        constexpr int C = decltype(mn)::value ? 17 : 9, R = decltype(mn)::value ? 8 : 16;  // blocks of a row, a warp's rows
+        static_assert(R * C > 128 && R * C <= 160, "five rounds of 32 lanes");
+        q += R * lw * ld;
+        rows -= R * lw;
+        to += (uint32_t)(R * lw * C * 16);
+        if (rows >= R && len >= 16 * C && q >= lo + 15) {  // all there: the usual case, in little code
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = r0 + 32 * j;
-          v[j].load(p + r * ld + 16 * c, r < rows ? min(16, len - 16 * c) : 0, lo, hi);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = r0 + 32 * j;
-          v[j].store(dst + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)), r < rows ? min(16, len - 16 * c) : 0,
-                     ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)ld) & 15u);
-        }
-      };
-      // M- or N-major: contracted row (lt >> 4) + 16 j of 64, piece lt & 15 of
-      // 256 bytes of values (two panels); `rows` there are, `len` bytes of each
-      auto mn_major = [&](uint32_t dst, const char* p, long long ld, int rows, int len, const char* lo, const char* hi) {
-        const int c = lt & 15, r0 = lt >> 4;
-        GuPiece v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = r0 + 16 * j;
-          v[j].load(p + r * ld + 16 * c, r < rows ? min(16, len - 16 * c) : 0, lo, hi);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = r0 + 16 * j;
-          v[j].store(dst + (uint32_t)((c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                     r < rows ? min(16, len - 16 * c) : 0,
-                     ((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)ld) & 15u);
-        }
-      };
-      GuItem it;
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      while (ok && copy_item(it, false)) {
-        if (it.kind == GU_ZEROS) continue;
-        const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
-        const int mv = min(128, it.mv - (int)rank * 128), nv = min(half, it.nv - (int)rank * half);
-        const char* we = w_lo + (long long)it.e * g.n_out * g.n_in * ES;
-        const long long ldw = (long long)g.n_in * ES, ldr = g.ld_rows * ES, ldx = g.ld_x * ES;
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
-          if (!ok) break;
-          const uint32_t a = base + (uint32_t)(st * kStep), b = a + kGuTile;
-          const int k0 = kb * KE;
-          if constexpr (OP == G_MM) {
-            const int len = (g.n_in - k0) * ES;
-            if constexpr (ROWM) {
-              k_major(a, r_lo + m * ldr + k0 * ES, ldr, mv, len, r_lo, r_hi);
-              k_major(b, we + n * ldw + k0 * ES, ldw, nv, len, w_lo, w_hi);
-            } else {
-              k_major(a, we + m * ldw + k0 * ES, ldw, mv, len, w_lo, w_hi);
-              k_major(b, r_lo + n * ldr + k0 * ES, ldr, nv, len, r_lo, r_hi);
-            }
-          } else if constexpr (OP == G_DX) {
-            mn_major(a, we + k0 * ldw + m * ES, ldw, g.n_out - k0, mv * ES, w_lo, w_hi);
-            k_major(b, r_lo + n * ldr + k0 * ES, ldr, nv, (g.n_out - k0) * ES, r_lo, r_hi);
-          } else {
-            const int left = it.r1 - it.r0 - k0;
-            mn_major(a, r_lo + (long long)(it.r0 + k0) * ldr + m * ES, ldr, left, mv * ES, r_lo, r_hi);
-            mn_major(b, x_lo + (long long)(it.r0 + k0) * ldx + n * ES, ldx, left, nv * ES, x_lo, x_hi);
+          for (int k = 0; k < 5; ++k) {
+            const int i = lane + 32 * k;
+            const char* at = q + i / C * ld;
+            if (k < 4 || i < R * C) gu_fetch16(to + 16 * i, at - (reinterpret_cast<uintptr_t>(at) & 15) + 16 * (i % C));
           }
-          tc_fence_proxy();  // the stores, before the tensor core reads them
-          __syncwarp();
-          if (lane == 0) cl_arrive(cl_addr(full(st), 0));
-          if (++st == NS) st = 0, ph ^= 1u;
+        } else {
+#pragma unroll 1
+          for (int i = lane; i < R * C; i += 32) {
+            const char* at = q + i / C * ld;
+            gu_fetch16(to + 16 * i, at - (reinterpret_cast<uintptr_t>(at) & 15) + 16 * (i % C),
+                       i / C < rows && len > 0 ? at + len : lo, lo);
+          }
         }
+      };
+      // four pieces per thread: of one row, so that it reads each block once,
+      // and neighbouring lanes in neighbouring rows, which hit different banks
+      auto cut = [&](auto mn, uint32_t to, uint32_t from, uint32_t shift) {
+        constexpr int C = decltype(mn)::value ? 17 : 9, R = decltype(mn)::value ? 8 : 16;
+        const int r = R * lw + (lane & (R - 1)), c = lane / R * 4;
+        from += (uint32_t)((r * C + c) * 16);
+        to += (uint32_t)((c >> 3) * 8192 + r * 128);
+        uint4 x = tc_lds128(from);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 y = tc_lds128(from + 16 * (i + 1));
+          gu_cut16(to + (uint32_t)((((c & 7) + i) ^ (r & 7)) << 4), x, y, shift);
+          x = y;
+        }
+      };
+      constexpr std::integral_constant<bool, A_MN> a_mn;
+      constexpr std::integral_constant<bool, B_MN> b_mn;
+      GuItem it;
+      it.kb1 = 0;
+      int kb = 0;
+      const char *ap = nullptr, *bp = nullptr;  // the first byte of the next step
+      int a_rows = 0, b_rows = 0, a_len = 0, b_len = 0;
+      const int k_row = 16 * lw + (lane & 15), m_row = 8 * lw + (lane & 7);
+      uint32_t how = 0;  // shifts of A and B, whether this warp has rows of a K-major B
+      // (K-major: rows in M or N, bytes left in K; M- or N-major: the reverse)
+      constexpr uint32_t kNoStep = 0x10000, kNoMore = 0x20000;
+      auto next_step = [&](uint32_t to) -> uint32_t {
+        if (kb >= it.kb1) {
+          if (!copy_item(it, false)) return kNoMore;
+          kb = it.kind == GU_ZEROS ? it.kb1 : it.kb0;
+          // (a turn without a step: the steps before it are cut before another
+          // item is waited for, which may come only after their tile is done)
+          if (kb >= it.kb1) return kNoStep;
+          const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
+          const int mv = min(128, it.mv - (int)rank * 128), nv = min(half, it.nv - (int)rank * half);
+          const char* we = w_lo + (long long)it.e * g.n_out * ldw;
+          const int k0 = kb * KE;
+          if constexpr (OP == G_DW) {
+            ap = r_lo + (long long)(it.r0 + k0) * ldr + m * ES;
+            bp = x_lo + (long long)(it.r0 + k0) * ldx + n * ES;
+            a_rows = b_rows = it.r1 - it.r0 - k0;
+            a_len = (g.n_out - m) * ES;  // (what is beyond the tile is not stored)
+            b_len = (g.n_in - n) * ES;
+            how = ((uint32_t)((uintptr_t)ap + m_row * ldr) & 15) | ((uint32_t)((uintptr_t)bp + m_row * ldx) & 15) << 4 | 0x100u;
+          } else {
+            const char* wp = OP == G_DX ? we + k0 * ldw + m * ES : we + (long long)(ROWM ? n : m) * ldw + k0 * ES;
+            const char* rp = r_lo + (long long)(ROWM ? m : n) * ldr + k0 * ES;
+            const int k_len = ((OP == G_MM ? g.n_in : g.n_out) - k0) * ES;
+            ap = ROWM ? rp : wp;
+            bp = ROWM ? wp : rp;
+            a_rows = OP == G_DX ? g.n_out - k0 : mv;
+            a_len = OP == G_DX ? (g.n_in - m) * ES : k_len;
+            b_rows = nv;
+            b_len = k_len;
+            how = ((uint32_t)((uintptr_t)ap + (A_MN ? m_row : k_row) * (ROWM ? ldr : ldw)) & 15) |
+                  ((uint32_t)((uintptr_t)bp + k_row * (ROWM ? ldw : ldr)) & 15) << 4 | (16 * lw < half ? 0x100u : 0u);
+          }
+        }
+        const long long lda = OP == G_DW || ROWM ? ldr : ldw, ldb = OP == G_DW ? ldx : ROWM ? ldw : ldr;
+        fetch(a_mn, to, ap, lda, a_rows, a_len, OP == G_DW || ROWM ? r_lo : w_lo);
+        if (how & 0x100u) fetch(b_mn, to + kGuRaw, bp, ldb, b_rows, b_len, OP == G_DW ? x_lo : ROWM ? w_lo : r_lo);
+        if constexpr (A_MN) {
+          ap += 64 * lda;
+          a_rows -= 64;
+        } else {
+          ap += 128;
+          a_len -= 128;
+        }
+        if constexpr (B_MN) {
+          bp += 64 * ldb;
+          b_rows -= 64;
+        } else {
+          bp += 128;
+          b_len -= 128;
+        }
+        ++kb;
+        return how;
+      };
+      int st = 0, in = 0, out = 0, ahead = 0;
+      uint32_t ph = 0, last = 0, hows[kGuRaws - 1];
+      bool ok = true;
+      while (ok) {
+        // (a group of copies per turn, also where no step is left)
+        if (last != kNoMore) last = next_step(raw0 + (uint32_t)(in * 2 * kGuRaw));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++in == kGuRaws) in = 0;
+        const uint32_t now = hows[0];
+#pragma unroll
+        for (int i = 0; i + 2 < kGuRaws; ++i) hows[i] = hows[i + 1];
+        hows[kGuRaws - 2] = last;
+        if (ahead < kGuRaws - 1) {
+          ++ahead;
+          continue;
+        }
+        if (now == kNoMore) break;
+        const uint32_t raw = raw0 + (uint32_t)(out * 2 * kGuRaw);
+        if (++out == kGuRaws) out = 0;
+        if (now == kNoStep) continue;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGuRaws - 1) : "memory");
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
+        if (!ok) break;
+        const uint32_t a = base + (uint32_t)(st * kStep);
+        cut(a_mn, a, raw, now & 15u);
+        if (now & 0x100u) cut(b_mn, a + kGuTile, raw + kGuRaw, now >> 4 & 15u);
+        tc_fence_proxy();  // the stores, before the tensor core reads them
+        __syncwarp();
+        if (lane == 0) cl_arrive(cl_addr(full(st), 0));
+        if (++st == NS) st = 0, ph ^= 1u;
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     if constexpr (LDG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuLdgHigh));
