@@ -325,10 +325,10 @@ constexpr uint32_t kGuBarOff = kGuLineOff + sizeof(GuLine);
 constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
-template <int OP, bool FP8, bool ROWM, int MT_>
+template <int OP, bool FP8, bool ROWM, int MT_, bool LDG>
 struct GuTiles {
   static constexpr int MT = MT_;
-  static constexpr bool kRowsM = ROWM, kFp8 = FP8;
+  static constexpr bool kRowsM = ROWM, kFp8 = FP8, kLdg = LDG;
   static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
   static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
   // N values per MMA in multiples of 16 (8-bit: 32; dw: whole 64-value panels in both CTAs)
@@ -546,7 +546,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   // evenly, for at most as many pairs as there are, or all of it is the line,
   // whichever costs less.  Measured, in us, for tiles of np columns: a step
   // 0.145 + np / 3000 (8-bit of over 64 columns, which hand over every other
-  // step: 0.45); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
+  // step: 0.45; LDG: 0.8 + np / 250); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
   // steps of 32 columns: whole 33.0, in four 18.2, eight 17.2, sixteen 20.1; 19
   // steps of 240: whole 13.6, in two 20.7.  dw, whose tiles differ in length:
   // dealt if the longest are short, else the line.
@@ -563,7 +563,9 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       const int rows = l.off[p.E] - l.off[0], m_tiles = max(1, Tiles::m_count(p, rows));
       // columns of a tile, on average
       const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out) : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
-      const float step = Tiles::kFp8 && np > 64.f ? 0.45f : 0.145f + np * (1.f / 3000.f);
+      const float step = Tiles::kLdg                 ? 0.8f + np * (1.f / 250.f)
+                         : Tiles::kFp8 && np > 64.f ? 0.45f
+                                                    : 0.145f + np * (1.f / 3000.f);
       const float join = 0.4f + np * (1.f / 62.f), part = 0.2f + np * (1.f / 154.f);
       float best = r ? steps * step : 0.f;
       int k = 1;
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
   constexpr int F32 = FP8 || LDG ? -1 : CHAIN ? 1 : 0;
   constexpr int NS = LDG ? 2 : 12 / (MT + 1);  // stages
   constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
-  using Tiles = GuTiles<OP, FP8, ROWM, MT>;
+  using Tiles = GuTiles<OP, FP8, ROWM, MT, LDG>;
   using Walk = GuWalk<Tiles>;
   constexpr bool A_MN = OP != G_MM, B_MN = OP == G_DW;
   constexpr int KE = Tiles::KE;
