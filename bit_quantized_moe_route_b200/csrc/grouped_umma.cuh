@@ -780,6 +780,28 @@ MOE_DEV void gu_lines_out(void* out, long long base, long long ld, int left, int
   __syncwarp();
 }
 
+// Zeros to `vals` rows of `cols` (at most 128) values of es bytes.
+MOE_DEV void gu_zeros_out(char* o, long long ld, int cols, int vals, int es, int unit) {
+  const int lane = threadIdx.x & 31;
+  if (unit >= 16) {
+    const int wide = es == 4 ? 32 : 16, c = lane & (wide - 1), left = cols - c * (16 / es);  // 16-byte pieces of a row
+    const int step = 32 / wide;
+#pragma unroll 4
+    for (int r = lane / wide; r < vals; r += step) {
+      char* to = o + r * ld + 16 * c;
+      if (left >= 16 / es) *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+      else
+#pragma unroll 1
+        for (int i = 0; i < left * es; i += 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    }
+  } else {
+#pragma unroll 1
+    for (int r = 0; r < vals; ++r)
+#pragma unroll 1
+      for (int i = 2 * lane; i < cols * es; i += 64) *reinterpret_cast<uint16_t*>(o + r * ld + i) = 0;
+  }
+}
+
 // 32 bytes to a 32-byte aligned address: one whole sector per lane and store
 // (with 16 the lanes of a warp, each in a row of its own, fill half sectors)
 MOE_DEV void gu_st256(void* p, const uint32_t* w) {
@@ -1433,16 +1455,9 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
       };
       if (it.kind == GU_ZEROS) {
         for (int half = 0; half < it.halves; ++half) {
-          if constexpr (F32 == 0 && ROWM) {
-            uint32_t z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0;
-            for (int c = c_first; c < c_end; c += 2) out64(c, z);
-          } else {
-            float z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0.f;
-            for (int c = c_first; c < c_end; c += C_STEP) out32(c, z);
+          if constexpr (ROWM) {
+            const int cols = min(it.nv, 32 * c_end) - 32 * c_first;
+            gu_zeros_out(reinterpret_cast<char*>(g.out) + (ob + 32 * c_first) * out_bytes, ld * out_bytes, cols, vals, out_bytes, unit);
           }
           ob += ROWM ? 256 * ld : 256;
           vals = min(32, it.mv - 256 - m);
