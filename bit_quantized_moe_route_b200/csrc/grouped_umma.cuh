@@ -72,7 +72,10 @@
 // (commit, barriers of two CTAs, TMEM reads) against 512 for the MMA of a
 // 256-row tile, so a half of tensor memory holds one step of a wide tile, two
 // of a tile of up to 128 rows or four of up to 64, handed over together, and
-// is given back when its last values are in registers.
+// is given back when its last values are in registers.  With the rows on the
+// M side a thread holds 128 sums and 64 of a step's, of 208 registers: what
+// makes the compiler spill four bytes there costs a third (32,768 rows over 32
+// experts: 430 us, not 317).
 #pragma once
 
 #include <cuda.h>
@@ -267,9 +270,8 @@ MOE_DEV void gu_fetch16(uint32_t to, const char* from, const char* end, const ch
       asm volatile("{ .reg .b8 t; cvt.u8.u16 t, %1; st.shared.b8 [%0], t; }" ::"r"(to + i), "h"(x) : "memory");
     }
   } else {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(n > 0 ? from : lo - (reinterpret_cast<uintptr_t>(lo) & 15)),
-                 "r"(n)
-                 : "memory");
+    const char* src = n > 0 ? from : lo - (reinterpret_cast<uintptr_t>(lo) & 15);  // (of no bytes: any aligned address)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(n) : "memory");
   }
 }
 // the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
@@ -562,7 +564,8 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       const float steps = (float)Tiles::steps(p, 0);
       const int rows = l.off[p.E] - l.off[0], m_tiles = max(1, Tiles::m_count(p, rows));
       // columns of a tile, on average
-      const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out) : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
+      const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out)
+                                     : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
       const float step = Tiles::kLdg                 ? 0.8f + np * (1.f / 250.f)
                          : Tiles::kFp8 && np > 64.f ? 0.45f
                                                     : 0.145f + np * (1.f / 3000.f);
@@ -576,7 +579,8 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
           k = i;
         }
       }
-      const float line = steps * step * rest / cols + 1.5f * (join + 2.5f * part);
+      const float parts = fmaxf(1.f, (float)cols / max(1, rest)) + 1.5f;  // of a tile on the line
+      const float line = steps * step * rest / cols + 1.5f * (join + parts * part);
       if (q * steps * step + best <= line) {
         halves = q;
         each_in = k;
@@ -956,7 +960,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
       uint32_t ph = 0;
       bool ok = true;
       while (ok && copy_item(it, false)) {
-        if (it.kind == GU_ZEROS) continue;
+        if (OP == G_DW && it.kind == GU_ZEROS) continue;
         const int half = it.np >> 1;
         const int m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
         const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
@@ -1078,7 +1082,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             }
         };
         while (ok && copy_item(it, true)) {
-          if (it.kind == GU_ZEROS) continue;
+          if (OP == G_DW && it.kind == GU_ZEROS) continue;
           const uint32_t idesc = idesc0 | ((uint32_t)(it.np >> 3) << 17);
           if (MT > 1 && it.halves > 1) {
             // Both halves of the tile.  The second half's accumulator is still
@@ -1234,7 +1238,8 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
       const long long ldw = (long long)g.n_in * ES, ldr = g.ld_rows * ES, ldx = g.ld_x * ES;
       const uint32_t raw0 = base + NS * kStep;
       auto fetch = [&](auto mn, uint32_t to, const char* q, long long ld, int rows, int len, const char* lo) {
-        constexpr int C = decltype(mn)::value ? 17 : 9, R = decltype(mn)::value ? 8 : 16;  // blocks of a row, a warp's rows
+        constexpr int C = decltype(mn)::value ? 17 : 9;   // blocks of a row
+        constexpr int R = decltype(mn)::value ? 8 : 16;   // a warp's rows
         static_assert(R * C > 128 && R * C <= 160, "five rounds of 32 lanes");
         q += R * lw * ld;
         rows -= R * lw;
@@ -1298,7 +1303,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
             a_rows = b_rows = it.r1 - it.r0 - k0;
             a_len = (g.n_out - m) * ES;  // (what is beyond the tile is not stored)
             b_len = (g.n_in - n) * ES;
-            how = ((uint32_t)((uintptr_t)ap + m_row * ldr) & 15) | ((uint32_t)((uintptr_t)bp + m_row * ldx) & 15) << 4 | 0x100u;
+            how = 0x100u | ((uint32_t)((uintptr_t)ap + m_row * ldr) & 15) | ((uint32_t)((uintptr_t)bp + m_row * ldx) & 15) << 4;
           } else {
             const char* wp = OP == G_DX ? we + k0 * ldw + m * ES : we + (long long)(ROWM ? n : m) * ldw + k0 * ES;
             const char* rp = r_lo + (long long)(ROWM ? m : n) * ldr + k0 * ES;
@@ -1453,16 +1458,17 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
         const int left = it.nv - 32 * c;
         if (left > 0 && vals > 0) gu_lines_out<false, 128>(g.out, ob + 32 * c, ld, left, vals, unit, w, buf);
       };
-      if (it.kind == GU_ZEROS) {
-        for (int half = 0; half < it.halves; ++half) {
-          if constexpr (ROWM) {
-            const int cols = min(it.nv, 32 * c_end) - 32 * c_first;
-            gu_zeros_out(reinterpret_cast<char*>(g.out) + (ob + 32 * c_first) * out_bytes, ld * out_bytes, cols, vals, out_bytes, unit);
+      if constexpr (OP == G_DW) {
+        if (it.kind == GU_ZEROS) {
+          const int cols = min(it.nv, 32 * c_end) - 32 * c_first;
+          for (int half = 0; half < it.halves; ++half) {
+            char* o = reinterpret_cast<char*>(g.out) + (ob + 32 * c_first) * out_bytes;
+            gu_zeros_out(o, ld * out_bytes, cols, vals, out_bytes, unit);
+            ob += 256 * ld;
+            vals = min(32, it.mv - 256 - m);
           }
-          ob += ROWM ? 256 * ld : 256;
-          vals = min(32, it.mv - 256 - m);
+          continue;
         }
-        continue;
       }
       auto wait_sums = [&]() {
         const bool got = cl_bar_wait(acc_full(seg & (kGuSegs - 1)), (uint32_t)(seg / kGuSegs) & 1u, abort_flag);
