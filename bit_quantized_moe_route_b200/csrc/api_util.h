@@ -15,8 +15,8 @@ void api_clear_detail();
 // Device (or managed) memory, not NULL.
 moe_status_t api_check_dev_ptr(const void* p, const char* name);
 // Tiled tensor map of rank 2 or 3: dims and box in elements (dims[0] contiguous),
-// strides in bytes for dims 1.., 128-byte swizzle, zero fill out of bounds.
+// strides in bytes for dims 1.., 128-byte swizzle or none, zero fill out of bounds.
 moe_status_t api_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,
-                            const uint64_t* strides, const uint32_t* box);
+                            const uint64_t* strides, const uint32_t* box, bool swizzle = true);
 
 }  // namespace moe

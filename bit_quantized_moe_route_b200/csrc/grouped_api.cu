@@ -132,15 +132,41 @@ template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
   const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>();
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
-  GuParams q;
+  GuKernelParams<FP8, LDG> q;
   q.g = p;
   q.type = type;
   q.ws = reinterpret_cast<unsigned char*>(ws);
   q.split_most = 16;
-  if constexpr (!LDG) {
-    const uint64_t es = FP8 ? 1 : 2;
-    const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                       : type == G_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint64_t es = FP8 ? 1 : 2;
+  const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : type == G_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if constexpr (LDG) {
+    constexpr int R = GuLdgParams<FP8>::R;
+    // (a class that has no rows, as any without rows at all, is one value that may be read and is not used)
+    auto classes = [&](CUtensorMap* maps, const void* ptr, long long rows, int cols, long long ld, uint32_t block,
+                       uint32_t box_rows) -> moe_status_t {
+      if (rows < 1) ptr = ws;
+      for (int c = 0; c < R; ++c) {
+        const bool any = c < rows;
+        const uintptr_t at = (uintptr_t)ptr + (any ? c * ld * es : 0);
+        const uint64_t before = (at & 15) / es;
+        const uint64_t dims[2] = {before + (any ? cols : 1), any ? (uint64_t)((rows - c + R - 1) / R) : 1u};
+        const uint64_t st[1] = {(uint64_t)ld * es * R};
+        const uint32_t box[2] = {block / (uint32_t)es, box_rows / R};
+        GMM_TRY(api_tensor_map(&maps[c], dt, 2, (const void*)(at & ~(uintptr_t)15), dims, st, box, false));
+      }
+      return MOE_OK;
+    };
+    if constexpr (OP == G_DW) {
+      GMM_TRY(classes(q.a_rows, p.rows_in, p.rows, p.n_out, p.ld_rows, 272, 64));
+      GMM_TRY(classes(q.b_rows, p.x, p.rows, p.n_in, p.ld_x, 272, 64));
+    } else {
+      const int cols = OP == G_MM ? p.n_in : p.n_out;
+      GMM_TRY(classes(q.a_rows, p.w, (long long)p.E * p.n_out, p.n_in, p.n_in, OP == G_DX ? 272 : 144, OP == G_DX ? 64 : 128));
+      if (p.rows > 64) GMM_TRY(classes(q.b_rows, p.rows_in, p.rows, cols, p.ld_rows, 144, 128));
+      GMM_TRY(classes(q.b_few, p.rows_in, p.rows, cols, p.ld_rows, 144, 32));
+    }
+  } else {
     const uint32_t inner = 128 / es;
     if constexpr (OP == G_DW) {
       const uint64_t dims_x[2] = {(uint64_t)p.n_in, (uint64_t)p.rows}, st_x[1] = {(uint64_t)p.ld_x * es};

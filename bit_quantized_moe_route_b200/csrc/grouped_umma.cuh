@@ -93,6 +93,17 @@ constexpr int kGuRing = 12 * kGuTile;
 constexpr int kGuRaw = 128 * (128 + 16);  // (64 rows of 256 + 16 are less)
 constexpr int kGuRaws = 3;
 static_assert(2 * 2 * kGuTile + kGuRaws * 2 * kGuRaw <= kGuRing, "operand ring");
+// bytes from the blocks of one class of rows (their number modulo 16 or, for
+// 16-bit values, 8) to the next's; `few`: 32 rows, not 128.  TMA wants
+// multiples of 128.
+template <bool FP8>
+constexpr uint32_t gu_raw_class(bool mn, bool few) {
+  const int r = FP8 ? 16 : 8;
+  return mn ? 64 / r * 272 : few ? (32 / r * 144 + 127) / 128 * 128 : 128 / r * 144;
+}
+static_assert(gu_raw_class<false>(true, false) % 128 == 0 && gu_raw_class<false>(false, false) % 128 == 0 &&
+                  gu_raw_class<true>(false, false) % 128 == 0,
+              "TMA's alignment in shared memory");
 constexpr int kGuN = 256;                 // output rows per tile
 // Warps: 0 loads, 1 MMA, 2 scales, 3 items, 4-11 the epilogue, two for each 32
 // TMEM lanes.  (Sixteen epilogue warps were slower: each barrier wait and
@@ -137,6 +148,16 @@ struct alignas(64) GuParams {
   int split_most;        // pieces that a tile may be cut into
   unsigned char* ws;
 };
+
+// LDG: rows c, c + R, .. of an operand, from the aligned block that holds the
+// first byte of row c on (R rows are a multiple of 16 bytes apart).
+template <bool FP8>
+struct alignas(64) GuLdgParams : GuParams {
+  static constexpr int R = FP8 ? 16 : 8;
+  CUtensorMap a_rows[R], b_rows[R], b_few[R];  // b_few: of 32 rows, not 128
+};
+template <bool FP8, bool LDG>
+using GuKernelParams = std::conditional_t<LDG, GuLdgParams<FP8>, GuParams>;
 
 // ------------------------------------------------------------ PTX wrappers
 // 4-byte copy to shared memory, zero if not `in`
@@ -253,28 +274,7 @@ MOE_DEV void gu_times(unsigned long long (&acc)[16], const uint32_t (&r)[32], un
   for (int i = 0; i < 32; i += 2) gu_fma2(acc[i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
 }
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
-// LDG: 16 bytes from `from` (16-byte aligned) to shared memory, on their way
-MOE_DEV void gu_fetch16(uint32_t to, const char* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-// ... where those from `end` on are zeros and, like those before `lo` (the
-// operand's first byte), not read.
-MOE_DEV void gu_fetch16(uint32_t to, const char* from, const char* end, const char* lo) {
-  const long long left = end - from;
-  const uint32_t n = left >= 16 ? 16u : left > 0 ? (uint32_t)left : 0u;
-  if (from < lo && n > 0) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      const char* q = from + i;
-      const uint16_t x = q >= lo && q < end ? *reinterpret_cast<const uint8_t*>(q) : 0;
-      asm volatile("{ .reg .b8 t; cvt.u8.u16 t, %1; st.shared.b8 [%0], t; }" ::"r"(to + i), "h"(x) : "memory");
-    }
-  } else {
-    const char* src = n > 0 ? from : lo - (reinterpret_cast<uintptr_t>(lo) & 15);  // (of no bytes: any aligned address)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(n) : "memory");
-  }
-}
-// the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
+// LDG: the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
 MOE_DEV void gu_cut16(uint32_t to, uint4 a, uint4 b, uint32_t shift) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t t[6], u[5], o[4];
@@ -817,7 +817,8 @@ MOE_DEV void gu_st256(void* p, const uint32_t* w) {
 // ------------------------------------------------------------ the kernel
 // Launched in clusters of two CTAs (gridDim.x even), one CTA per SM.
 template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
-__global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const __grid_constant__ GuParams p) {
+__global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
+    const __grid_constant__ GuKernelParams<FP8, LDG> p) {
   constexpr int EW = kGuEpiWarps, H = EW / 4, SR = kGuStageRows;
   constexpr bool SCALE_RING = FP8 && !ROWM;  // the scales come through shared memory
   static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
@@ -847,7 +848,10 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
   constexpr int kBarIt = kBarSc + 2 * kGuScaleSlots;
   auto it_full = [&](int s) { return bar + 8u * (kBarIt + s); };                        // item warp
   auto it_empty = [&](int s) { return bar + 8u * (kBarIt + kGuItems + s); };            // this CTA's other warps
-  constexpr int kBars = kBarIt + 2 * kGuItems;
+  constexpr int kBarRaw = kBarIt + 2 * kGuItems;
+  auto raw_full = [&](int s) { return bar + 8u * (kBarRaw + s); };                      // LDG: TMA bytes
+  auto raw_empty = [&](int s) { return bar + 8u * (kBarRaw + kGuRaws + s); };           // LDG: load warps
+  constexpr int kBars = kBarRaw + (LDG ? 2 * kGuRaws : 0);
   const uint32_t drain = bar + 8u * kBars;                                              // (L)
   const uint32_t join = drain + 8u;                                                     // epilogue warps
   int* tail = reinterpret_cast<int*>(gen + kGuBarOff + 8 * (kBars + 2));
@@ -869,6 +873,11 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
       tc_bar_init(full(s), LDG ? 2 * kGuLoadWarps : 1);
       tc_bar_init(empty(s), 1);
     }
+    if constexpr (LDG)
+      for (int s = 0; s < kGuRaws; ++s) {
+        tc_bar_init(raw_full(s), 1);
+        tc_bar_init(raw_empty(s), kGuLoadWarps);
+      }
     for (int b = 0; b < kGuSegs; ++b) {
       tc_bar_init(acc_full(b), 1);
       tc_bar_init(acc_empty(b), 2 * EW);
@@ -879,7 +888,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
     }
     for (int s = 0; s < kGuItems; ++s) {
       tc_bar_init(it_full(s), 1);
-      tc_bar_init(it_empty(s), (LDG ? kGuLoadWarps : 1) + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
+      tc_bar_init(it_empty(s), (LDG ? 1 + kGuLoadWarps : 1) + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
     }
     tc_bar_init(drain, 1);
     tc_bar_init(join, EW);
@@ -947,7 +956,49 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
     if constexpr (LDG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLow));
     else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
     if (LDG && warp == 0) {
-      // (the load warps bring the operands)
+      if constexpr (LDG) {
+        // ================= TMA issuer of the aligned blocks: lanes 0 .. R - 1
+        // the rows of A by their number modulo R, lanes 16 .. 16 + R - 1 those of B
+        constexpr int R = GuLdgParams<FP8>::R;
+        const int c = lane & 15;
+        const bool is_b = lane >= 16, mine = c < R;
+        const bool mn = is_b ? B_MN : A_MN;
+        GuItem it;
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        while (ok && copy_item(it, false)) {
+          if (OP == G_DW && it.kind == GU_ZEROS) continue;
+          const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
+          const bool few = !B_MN && half <= 32;
+          const CUtensorMap* map = is_b ? (few ? &p.b_few[c & (R - 1)] : &p.b_rows[c & (R - 1)]) : &p.a_rows[c & (R - 1)];
+          // the first step's first row (of the whole operand) and value
+          const int k0 = it.kb0 * KE, we = it.e * g.n_out;
+          int row = OP == G_DW ? it.r0 + k0 : is_b ? n : OP == G_DX ? we + k0 : we + m;
+          int x = mn ? (is_b ? n : m) : k0;
+          const uint32_t to = (is_b ? (uint32_t)kGuRaw : 0u) + (uint32_t)c * gu_raw_class<FP8>(mn, is_b && few);
+          const uint32_t bytes = (A_MN ? 64 * 272 : 128 * 144) + (B_MN ? 64 * 272 : few ? 32 * 144 : 128 * 144);
+          for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            ok = __all_sync(0xffffffffu, cl_bar_wait(raw_empty(st), ph ^ 1u, abort_flag)) != 0;
+            if (!ok) break;
+            if (lane == 0) um_expect_tx(raw_full(st), bytes);
+            __syncwarp();
+            if (mine)
+              um_tma_2d(base + (uint32_t)(NS * kStep + st * 2 * kGuRaw) + to, map, x, (row - c + R - 1) / R, raw_full(st));
+            if (mn) row += 64;
+            else x += KE;
+            ++issued;
+            if (++st == kGuRaws) st = 0, ph ^= 1u;
+          }
+        }
+        // copies that no load warp will wait for (after a timeout) land before the block ends
+        if (!ok || *abort_flag) {
+          const long long t0 = clock64();
+          for (int i = max(0, issued - kGuRaws); i < issued; ++i)
+            while (!cl_bar_try(raw_full(i % kGuRaws), (uint32_t)(i / kGuRaws) & 1u) && clock64() - t0 < kTcWaitCycles) {
+            }
+        }
+      }
     } else if (warp == 0) {
       // ================= TMA issuer of this CTA's halves of both operands
       // (lane 0; all lanes share the many small copies of dw's last steps)
@@ -1222,155 +1273,65 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(const 
     }
   } else if (LDG && warp >= 4 + kGuEpiWarps) {
     if constexpr (LDG) {
-      // ================= loads of any alignment: the aligned blocks that hold
-      // a step's rows, kGuRaws - 1 steps ahead of the cutting: for each of the
-      // 128 rows of a K-major operand nine blocks for 128 bytes, for each of
-      // the 64 contracted rows of an M- or N-major one 17 for 256 bytes of
-      // values (two panels).  A warp cuts the rows that it has loaded itself.
-      // (What precedes a row's first byte in its block is the same for all
-      // steps of an item: they are multiples of 16 bytes apart.)
+      // ================= the operands' pieces out of the aligned blocks: eight
+      // neighbouring lanes have one row's 128 bytes (which hit different banks,
+      // read and written); M- or N-major: of 64 rows, each of two panels.
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLoad));
-      constexpr int ES = FP8 ? 1 : 2;
+      constexpr int ES = FP8 ? 1 : 2, R = GuLdgParams<FP8>::R;
       const int lw = warp - 4 - kGuEpiWarps;  // 0 .. 7
-      const char* w_lo = reinterpret_cast<const char*>(g.w);
-      const char* r_lo = reinterpret_cast<const char*>(g.rows_in);
-      const char* x_lo = reinterpret_cast<const char*>(g.x);
-      const long long ldw = (long long)g.n_in * ES, ldr = g.ld_rows * ES, ldx = g.ld_x * ES;
-      const uint32_t raw0 = base + NS * kStep;
-      auto fetch = [&](auto mn, uint32_t to, const char* q, long long ld, int rows, int len, const char* lo) {
-        constexpr int C = decltype(mn)::value ? 17 : 9;   // blocks of a row
-        constexpr int R = decltype(mn)::value ? 8 : 16;   // a warp's rows
-        static_assert(R * C > 128 && R * C <= 160, "five rounds of 32 lanes");
-        q += R * lw * ld;
-        rows -= R * lw;
-        to += (uint32_t)(R * lw * C * 16);
-        if (rows >= R && len >= 16 * C && q >= lo + 15) {  // all there: the usual case, in little code
-#pragma unroll
-          for (int k = 0; k < 5; ++k) {
-            const int i = lane + 32 * k;
-            const char* at = q + i / C * ld;
-            if (k < 4 || i < R * C) gu_fetch16(to + 16 * i, at - (reinterpret_cast<uintptr_t>(at) & 15) + 16 * (i % C));
-          }
-        } else {
-#pragma unroll 1
-          for (int i = lane; i < R * C; i += 32) {
-            const char* at = q + i / C * ld;
-            gu_fetch16(to + 16 * i, at - (reinterpret_cast<uintptr_t>(at) & 15) + 16 * (i % C),
-                       i / C < rows && len > 0 ? at + len : lo, lo);
-          }
-        }
-      };
-      // four pieces per thread: of one row, so that it reads each block once,
-      // and neighbouring lanes in neighbouring rows, which hit different banks
-      auto cut = [&](auto mn, uint32_t to, uint32_t from, uint32_t shift) {
-        constexpr int C = decltype(mn)::value ? 17 : 9, R = decltype(mn)::value ? 8 : 16;
-        const int r = R * lw + (lane & (R - 1)), c = lane / R * 4;
-        from += (uint32_t)((r * C + c) * 16);
-        to += (uint32_t)((c >> 3) * 8192 + r * 128);
-        uint4 x = tc_lds128(from);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 y = tc_lds128(from + 16 * (i + 1));
-          gu_cut16(to + (uint32_t)((((c & 7) + i) ^ (r & 7)) << 4), x, y, shift);
-          x = y;
+      // rows from number `first` on, of which the first is at `low` modulo 16 bytes
+      auto cut = [&](auto mn, uint32_t to, uint32_t from, uint32_t low, uint32_t ld, int first, int rows, uint32_t cls) {
+        constexpr bool MN = decltype(mn)::value;
+        constexpr int C = MN ? 16 : 8, PITCH = MN ? 272 : 144, J = 32 / C;  // pieces of a row, rows at a time
+        const int c = lane & (C - 1);
+#pragma unroll 2
+        for (int j = 0; j < 4; ++j) {
+          const int r = (16 / (C / 8)) * lw + lane / C + J * j;
+          if (!MN && r - lane / C >= rows) break;
+          const uint32_t at = from + (uint32_t)((first + r) & (R - 1)) * cls + (uint32_t)(r / R * PITCH + 16 * c);
+          const uint32_t dst = to + (uint32_t)((c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          if (!MN || r < rows) gu_cut16(dst, tc_lds128(at), tc_lds128(at + 16), (low + (uint32_t)r * ld) & 15u);
+          else tc_sts128(dst, 0u, 0u, 0u, 0u);
         }
       };
       constexpr std::integral_constant<bool, A_MN> a_mn;
       constexpr std::integral_constant<bool, B_MN> b_mn;
       GuItem it;
-      it.kb1 = 0;
-      int kb = 0;
-      const char *ap = nullptr, *bp = nullptr;  // the first byte of the next step
-      int a_rows = 0, b_rows = 0, a_len = 0, b_len = 0;
-      const int k_row = 16 * lw + (lane & 15), m_row = 8 * lw + (lane & 7);
-      uint32_t how = 0;  // shifts of A and B, whether this warp has rows of a K-major B
-      // (K-major: rows in M or N, bytes left in K; M- or N-major: the reverse)
-      constexpr uint32_t kNoStep = 0x10000, kNoMore = 0x20000;
-      auto next_step = [&](uint32_t to) -> uint32_t {
-        if (kb >= it.kb1) {
-          if (!copy_item(it, false)) return kNoMore;
-          kb = it.kind == GU_ZEROS ? it.kb1 : it.kb0;
-          // (a turn without a step: the steps before it are cut before another
-          // item is waited for, which may come only after their tile is done)
-          if (kb >= it.kb1) return kNoStep;
-          const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
-          const int mv = min(128, it.mv - (int)rank * 128), nv = min(half, it.nv - (int)rank * half);
-          const char* we = w_lo + (long long)it.e * g.n_out * ldw;
-          const int k0 = kb * KE;
-          if constexpr (OP == G_DW) {
-            ap = r_lo + (long long)(it.r0 + k0) * ldr + m * ES;
-            bp = x_lo + (long long)(it.r0 + k0) * ldx + n * ES;
-            a_rows = b_rows = it.r1 - it.r0 - k0;
-            a_len = (g.n_out - m) * ES;  // (what is beyond the tile is not stored)
-            b_len = (g.n_in - n) * ES;
-            how = 0x100u | ((uint32_t)((uintptr_t)ap + m_row * ldr) & 15) | ((uint32_t)((uintptr_t)bp + m_row * ldx) & 15) << 4;
-          } else {
-            const char* wp = OP == G_DX ? we + k0 * ldw + m * ES : we + (long long)(ROWM ? n : m) * ldw + k0 * ES;
-            const char* rp = r_lo + (long long)(ROWM ? m : n) * ldr + k0 * ES;
-            const int k_len = ((OP == G_MM ? g.n_in : g.n_out) - k0) * ES;
-            ap = ROWM ? rp : wp;
-            bp = ROWM ? wp : rp;
-            a_rows = OP == G_DX ? g.n_out - k0 : mv;
-            a_len = OP == G_DX ? (g.n_in - m) * ES : k_len;
-            b_rows = nv;
-            b_len = k_len;
-            how = ((uint32_t)((uintptr_t)ap + (A_MN ? m_row : k_row) * (ROWM ? ldr : ldw)) & 15) |
-                  ((uint32_t)((uintptr_t)bp + k_row * (ROWM ? ldw : ldr)) & 15) << 4 | (16 * lw < half ? 0x100u : 0u);
-          }
-        }
-        const long long lda = OP == G_DW || ROWM ? ldr : ldw, ldb = OP == G_DW ? ldx : ROWM ? ldw : ldr;
-        fetch(a_mn, to, ap, lda, a_rows, a_len, OP == G_DW || ROWM ? r_lo : w_lo);
-        if (how & 0x100u) fetch(b_mn, to + kGuRaw, bp, ldb, b_rows, b_len, OP == G_DW ? x_lo : ROWM ? w_lo : r_lo);
-        if constexpr (A_MN) {
-          ap += 64 * lda;
-          a_rows -= 64;
-        } else {
-          ap += 128;
-          a_len -= 128;
-        }
-        if constexpr (B_MN) {
-          bp += 64 * ldb;
-          b_rows -= 64;
-        } else {
-          bp += 128;
-          b_len -= 128;
-        }
-        ++kb;
-        return how;
-      };
-      int st = 0, in = 0, out = 0, ahead = 0;
-      uint32_t ph = 0, last = 0, hows[kGuRaws - 1];
+      int st = 0, rs = 0;
+      uint32_t ph = 0, rph = 0;
       bool ok = true;
-      while (ok) {
-        // (a group of copies per turn, also where no step is left)
-        if (last != kNoMore) last = next_step(raw0 + (uint32_t)(in * 2 * kGuRaw));
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (++in == kGuRaws) in = 0;
-        const uint32_t now = hows[0];
-#pragma unroll
-        for (int i = 0; i + 2 < kGuRaws; ++i) hows[i] = hows[i + 1];
-        hows[kGuRaws - 2] = last;
-        if (ahead < kGuRaws - 1) {
-          ++ahead;
-          continue;
+      while (ok && copy_item(it, false)) {
+        if (OP == G_DW && it.kind == GU_ZEROS) continue;
+        const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
+        const bool few = !B_MN && half <= 32;
+        const int k0 = it.kb0 * KE, we = it.e * g.n_out;
+        // numbers of the rows as the issuer has them, addresses and row strides modulo 16 bytes
+        int a_row = OP == G_DW ? it.r0 + k0 : OP == G_DX ? we + k0 : we + m, b_row = OP == G_DW ? it.r0 + k0 : n;
+        int left = OP == G_DW ? it.r1 - it.r0 - k0 : g.n_out - k0;  // contracted rows (M- or N-major)
+        const uint32_t lda = (uint32_t)(OP == G_DW ? g.ld_rows : g.n_in) * ES, ldb = (uint32_t)(OP == G_DW ? g.ld_x : g.ld_rows) * ES;
+        const uint32_t a_low = (uint32_t)reinterpret_cast<uintptr_t>(OP == G_DW ? g.rows_in : g.w) + (uint32_t)a_row * lda;
+        const uint32_t b_low = (uint32_t)reinterpret_cast<uintptr_t>(OP == G_DW ? g.x : g.rows_in) + (uint32_t)b_row * ldb;
+        const uint32_t a_cls = gu_raw_class<FP8>(A_MN, false), b_cls = gu_raw_class<FP8>(B_MN, few);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, cl_bar_wait(raw_full(rs), rph, abort_flag) &&
+                                           cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
+          if (!ok) break;
+          const uint32_t a = base + (uint32_t)(st * kStep), raw = base + (uint32_t)(NS * kStep + rs * 2 * kGuRaw);
+          cut(a_mn, a, raw, a_low, lda, a_row, A_MN ? left : 128, a_cls);
+          cut(b_mn, a + kGuTile, raw + kGuRaw, b_low, ldb, b_row, B_MN ? left : half, b_cls);
+          if (A_MN) a_row += 64;
+          if (B_MN) b_row += 64;
+          left -= 64;
+          tc_fence_proxy();  // the stores, before the tensor core reads them
+          __syncwarp();
+          if (lane == 0) {
+            cl_arrive(cl_addr(full(st), 0));
+            tc_bar_arrive(raw_empty(rs));
+          }
+          if (++st == NS) st = 0, ph ^= 1u;
+          if (++rs == kGuRaws) rs = 0, rph ^= 1u;
         }
-        if (now == kNoMore) break;
-        const uint32_t raw = raw0 + (uint32_t)(out * 2 * kGuRaw);
-        if (++out == kGuRaws) out = 0;
-        if (now == kNoStep) continue;
-        asm volatile("cp.async.wait_group %0;" ::"n"(kGuRaws - 1) : "memory");
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, cl_bar_wait(empty(st), ph ^ 1u, abort_flag)) != 0;
-        if (!ok) break;
-        const uint32_t a = base + (uint32_t)(st * kStep);
-        cut(a_mn, a, raw, now & 15u);
-        if (now & 0x100u) cut(b_mn, a + kGuTile, raw + kGuRaw, now >> 4 & 15u);
-        tc_fence_proxy();  // the stores, before the tensor core reads them
-        __syncwarp();
-        if (lane == 0) cl_arrive(cl_addr(full(st), 0));
-        if (++st == NS) st = 0, ph ^= 1u;
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     if constexpr (LDG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuLdgHigh));

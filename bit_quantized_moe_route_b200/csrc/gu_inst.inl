@@ -29,7 +29,7 @@ template <>
 bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>(const GuParams& p, int pairs, cudaStream_t s) {
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
-  return cudaLaunchKernelEx(&cfg, gu_kernel, p) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, gu_kernel, static_cast<const GuKernelParams<GU_FP8, GU_LDG>&>(p)) == cudaSuccess;
 }
 
 template <>

@@ -1581,7 +1581,7 @@ void api_clear_detail() { g_detail[0] = 0; }
 moe_status_t api_check_dev_ptr(const void* p, const char* name) { return check_dev_ptr(p, name); }
 
 moe_status_t api_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,
-                            const uint64_t* strides, const uint32_t* box) {
+                            const uint64_t* strides, const uint32_t* box, bool swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t d[3], s[2];
@@ -1593,7 +1593,7 @@ moe_status_t api_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, co
     if (i) s[i - 1] = strides[i - 1];
   }
   const CUresult r = enc(m, dt, (cuuint32_t)rank, const_cast<void*>(ptr), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return MOE_OK;

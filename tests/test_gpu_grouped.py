@@ -641,3 +641,18 @@ def test_training_step(cuda_device, ws):
     _, mag = reference("dw", dy, x, off, 4)
     close(dw, w64.grad, mag, 48)
     assert moe.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("n_in,n_out", [(65, 129), (79, 1343), (1031, 77), (72, 2047)])
+def test_any_alignment_items(cuda_device, ws, op, n_in, n_out):
+    """Tiles of one step and experts without rows in a row, tiles of many, in operands that start anywhere."""
+    counts = [1, 0, 0, 0, 0, 0, 0, 2, 0, 0, 0, 300, 0, 1, 0, 0, 0, 0, 0, 37]
+    for shift, ld_pad in ((0, 0), (1, 0), (7, 3)):
+        run_op(op, counts, n_in, n_out, BF, FP if shift else BF, cuda_device, ws, ld_pad=ld_pad, shift=shift, pad=5)
+
+
+@pytest.mark.parametrize("n_in,n_out", [(127, 65), (1000, 300), (129, 2047)])
+def test_fp8_any_alignment_items(cuda_device, ws, n_in, n_out):
+    for shift, ld_pad in ((0, 0), (1, 0), (9, 5)):
+        run_fp8([1, 0, 0, 0, 0, 0, 2, 0, 200, 0, 1, 70], n_in, n_out, BF, cuda_device, ws, ld_pad=ld_pad, shift=shift, pad=2)
