@@ -103,14 +103,14 @@ moe_status_t check_gmm_ws(void* ws, size_t ws_bytes) {
 }
 
 // Resident pairs of a tensor-memory kernel on the current device (0: none).
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 int resident_pairs() {
   static std::atomic<int> cached[64];  // pairs + 1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = cached[dev].load(std::memory_order_acquire);
   if (!v) {
-    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>() + 1;
+    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>() + 1;
     cached[dev].store(v, std::memory_order_release);
   }
   return v - 1;
@@ -128,11 +128,11 @@ bool tma_ok(const GmmProblem& p, int es) {
 // The 8-bit product has its rows on the M side from this mean per expert on.
 constexpr long long kRowsPerExpertM = 192;
 
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
-  const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>();
+  const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>();
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
-  GuKernelParams<FP8, LDG> q;
+  GuKernelParams<FP8, ANY> q;
   q.g = p;
   q.type = type;
   q.ws = reinterpret_cast<unsigned char*>(ws);
@@ -140,8 +140,8 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
   const uint64_t es = FP8 ? 1 : 2;
   const CUtensorMapDataType dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : type == G_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if constexpr (LDG) {
-    constexpr int R = GuLdgParams<FP8>::R;
+  if constexpr (ANY) {
+    constexpr int R = GuAnyParams<FP8>::R;
     // (a class that has no rows, as any without rows at all, is one value that may be read and is not used)
     auto classes = [&](CUtensorMap* maps, const void* ptr, long long rows, int cols, long long ld, uint32_t block,
                        uint32_t box_rows) -> moe_status_t {
@@ -190,7 +190,7 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
       }
     }
   }
-  if (!gu_launch<OP, FP8, ROWM, MT, CHAIN, LDG>(q, pairs, s))
+  if (!gu_launch<OP, FP8, ROWM, MT, CHAIN, ANY>(q, pairs, s))
     return api_fail(MOE_ERR_CUDA, "grouped_umma_kernel: %s", cudaGetErrorString(cudaGetLastError()));
   return MOE_OK;
 }

@@ -34,12 +34,17 @@
 // comes from beyond the tensor's end, which TMA fills with zeros, so that no
 // value of another expert's rows (a NaN, say) enters a product.
 //
-// LDG: operands of any alignment and row stride, which TMA cannot read.  Eight
-// more warps copy the 16-byte aligned blocks that hold each step's rows to
-// shared memory, three steps at a time on their way (asynchronous copies: no
-// register waits; zeros beyond the matrix or the expert's rows), cut the
-// operands' 16-byte pieces out of two neighbouring blocks each and store them
-// where TMA would have put them.
+// ANY: operands of any alignment and row stride.  TMA takes 16-byte aligned
+// rows whose strides are multiples of 16 bytes, and 8 rows (e4m3: 16) are that
+// far apart whatever one row's stride is: each operand has 8 (16) tensor maps,
+// one for the rows of each number modulo 8, from the aligned block on that
+// holds its first row's first byte.  They bring the aligned blocks that hold a
+// step's rows to shared memory, three steps at a time on their way; eight more
+// warps cut the operands' 16-byte pieces out of two neighbouring blocks each
+// and store them where TMA would have put them, for two operand stages.  Bound
+// by those warps' shared memory traffic: 32,768 rows over 32 experts with 2,047
+// inputs run at 628 TFLOP/s (mm), 558 (dx), 542 (dw) and 429 (8-bit); with
+// asynchronous 16-byte copies instead of TMA it was 382, 344, 354 and 422.
 //
 // The tiles, in the order expert, M tile, row tile, are dealt out to the pairs
 // of CTAs in turn, so that pairs that run at the same time read the same
@@ -89,7 +94,7 @@ namespace moe {
 
 constexpr int kGuTile = 16384;            // bytes of 128 operand rows of one step
 constexpr int kGuRing = 12 * kGuTile;
-// LDG: two stages, and the aligned blocks of three steps
+// ANY: two stages, and the aligned blocks of three steps
 constexpr int kGuRaw = 128 * (128 + 16);  // (64 rows of 256 + 16 are less)
 constexpr int kGuRaws = 3;
 static_assert(2 * 2 * kGuTile + kGuRaws * 2 * kGuRaw <= kGuRing, "operand ring");
@@ -115,15 +120,15 @@ constexpr int kGuStageRows = 16;          // output rows that a warp stores toge
 // Registers per thread at launch and, where the epilogue holds a tile's sums or
 // rounded outputs, then of warps 0-3 and of the epilogue.
 constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
-// LDG: eight more warps; less for each.
+// ANY: eight more warps; less for each.
 constexpr int kGuLoadWarps = 8;
-constexpr int gu_threads(bool ldg) { return kGuThreads + (ldg ? 32 * kGuLoadWarps : 0); }
-constexpr int kGuLdgRegs = 96, kGuLdgLow = 64, kGuLdgLoad = 80, kGuLdgHigh = 128;
-static_assert(128 * kGuLdgLow + 32 * kGuLoadWarps * kGuLdgLoad + 32 * kGuEpiWarps * kGuLdgHigh <= gu_threads(true) * kGuLdgRegs,
+constexpr int gu_threads(bool any) { return kGuThreads + (any ? 32 * kGuLoadWarps : 0); }
+constexpr int kGuAnyRegs = 96, kGuAnyLow = 64, kGuAnyLoad = 64, kGuAnyHigh = 144;
+static_assert(128 * kGuAnyLow + 32 * kGuLoadWarps * kGuAnyLoad + 32 * kGuEpiWarps * kGuAnyHigh <= gu_threads(true) * kGuAnyRegs,
               "registers of the block");
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
-constexpr int gu_launch_regs(bool ldg) { return ldg ? kGuLdgRegs : kGuRegs; }
+constexpr int gu_launch_regs(bool any) { return any ? kGuAnyRegs : kGuRegs; }
 constexpr int kGuScaleSlots = 5;
 constexpr int kGuScaleAhead = 4;          // slots whose copies are in flight
 constexpr int kGuItems = 4;               // items handed out ahead
@@ -149,15 +154,15 @@ struct alignas(64) GuParams {
   unsigned char* ws;
 };
 
-// LDG: rows c, c + R, .. of an operand, from the aligned block that holds the
+// ANY: rows c, c + R, .. of an operand, from the aligned block that holds the
 // first byte of row c on (R rows are a multiple of 16 bytes apart).
 template <bool FP8>
-struct alignas(64) GuLdgParams : GuParams {
+struct alignas(64) GuAnyParams : GuParams {
   static constexpr int R = FP8 ? 16 : 8;
   CUtensorMap a_rows[R], b_rows[R], b_few[R];  // b_few: of 32 rows, not 128
 };
-template <bool FP8, bool LDG>
-using GuKernelParams = std::conditional_t<LDG, GuLdgParams<FP8>, GuParams>;
+template <bool FP8, bool ANY>
+using GuKernelParams = std::conditional_t<ANY, GuAnyParams<FP8>, GuParams>;
 
 // ------------------------------------------------------------ PTX wrappers
 // 4-byte copy to shared memory, zero if not `in`
@@ -274,7 +279,7 @@ MOE_DEV void gu_times(unsigned long long (&acc)[16], const uint32_t (&r)[32], un
   for (int i = 0; i < 32; i += 2) gu_fma2(acc[i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), s);
 }
 MOE_DEV void gu_add2(unsigned long long& c, unsigned long long a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
-// LDG: the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
+// ANY: the 16 bytes from byte `shift` of two blocks on, to where TMA would put them
 MOE_DEV void gu_cut16(uint32_t to, uint4 a, uint4 b, uint32_t shift) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t t[6], u[5], o[4];
@@ -327,10 +332,10 @@ constexpr uint32_t kGuBarOff = kGuLineOff + sizeof(GuLine);
 constexpr size_t gu_smem() { return 1024 + kGuBarOff + 512; }
 static_assert(gu_smem() <= 227 * 1024, "shared memory");
 
-template <int OP, bool FP8, bool ROWM, int MT_, bool LDG>
+template <int OP, bool FP8, bool ROWM, int MT_, bool ANY>
 struct GuTiles {
   static constexpr int MT = MT_;
-  static constexpr bool kRowsM = ROWM, kFp8 = FP8, kLdg = LDG;
+  static constexpr bool kRowsM = ROWM, kFp8 = FP8, kAny = ANY;
   static constexpr int KE = FP8 ? 128 : 64;                     // contracted values per step
   static constexpr int kMost = FP8 && !ROWM ? 128 : kGuN;       // N values per tile
   // N values per MMA in multiples of 16 (8-bit: 32; dw: whole 64-value panels in both CTAs)
@@ -548,7 +553,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   // evenly, for at most as many pairs as there are, or all of it is the line,
   // whichever costs less.  Measured, in us, for tiles of np columns: a step
   // 0.145 + np / 3000 (8-bit of over 64 columns, which hand over every other
-  // step: 0.45; LDG: 0.8 + np / 250); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
+  // step: 0.45; ANY: 0.45 + np / 470); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
   // steps of 32 columns: whole 33.0, in four 18.2, eight 17.2, sixteen 20.1; 19
   // steps of 240: whole 13.6, in two 20.7.  dw, whose tiles differ in length:
   // dealt if the longest are short, else the line.
@@ -566,7 +571,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       // columns of a tile, on average
       const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out)
                                      : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
-      const float step = Tiles::kLdg                 ? 0.8f + np * (1.f / 250.f)
+      const float step = Tiles::kAny                 ? 0.45f + np * (1.f / 470.f)
                          : Tiles::kFp8 && np > 64.f ? 0.45f
                                                     : 0.145f + np * (1.f / 3000.f);
       const float join = 0.4f + np * (1.f / 62.f), part = 0.2f + np * (1.f / 154.f);
@@ -816,18 +821,18 @@ MOE_DEV void gu_st256(void* p, const uint32_t* w) {
 
 // ------------------------------------------------------------ the kernel
 // Launched in clusters of two CTAs (gridDim.x even), one CTA per SM.
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
-__global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
-    const __grid_constant__ GuKernelParams<FP8, LDG> p) {
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
+__global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
+    const __grid_constant__ GuKernelParams<FP8, ANY> p) {
   constexpr int EW = kGuEpiWarps, H = EW / 4, SR = kGuStageRows;
   constexpr bool SCALE_RING = FP8 && !ROWM;  // the scales come through shared memory
   static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
-  static_assert(MT == 1 || (CHAIN == 0 && !LDG), "register sums and loads hold one MMA's");
+  static_assert(MT == 1 || (CHAIN == 0 && !ANY), "register sums and loads hold one MMA's");
   // what the kernel knows of the output's type: 1 fp32, 0 16 bits, -1 nothing
-  constexpr int F32 = FP8 || LDG ? -1 : CHAIN ? 1 : 0;
-  constexpr int NS = LDG ? 2 : 12 / (MT + 1);  // stages
+  constexpr int F32 = FP8 || ANY ? -1 : CHAIN ? 1 : 0;
+  constexpr int NS = ANY ? 2 : 12 / (MT + 1);  // stages
   constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
-  using Tiles = GuTiles<OP, FP8, ROWM, MT, LDG>;
+  using Tiles = GuTiles<OP, FP8, ROWM, MT, ANY>;
   using Walk = GuWalk<Tiles>;
   constexpr bool A_MN = OP != G_MM, B_MN = OP == G_DW;
   constexpr int KE = Tiles::KE;
@@ -849,9 +854,9 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
   auto it_full = [&](int s) { return bar + 8u * (kBarIt + s); };                        // item warp
   auto it_empty = [&](int s) { return bar + 8u * (kBarIt + kGuItems + s); };            // this CTA's other warps
   constexpr int kBarRaw = kBarIt + 2 * kGuItems;
-  auto raw_full = [&](int s) { return bar + 8u * (kBarRaw + s); };                      // LDG: TMA bytes
-  auto raw_empty = [&](int s) { return bar + 8u * (kBarRaw + kGuRaws + s); };           // LDG: load warps
-  constexpr int kBars = kBarRaw + (LDG ? 2 * kGuRaws : 0);
+  auto raw_full = [&](int s) { return bar + 8u * (kBarRaw + s); };                      // ANY: TMA bytes
+  auto raw_empty = [&](int s) { return bar + 8u * (kBarRaw + kGuRaws + s); };           // ANY: load warps
+  constexpr int kBars = kBarRaw + (ANY ? 2 * kGuRaws : 0);
   const uint32_t drain = bar + 8u * kBars;                                              // (L)
   const uint32_t join = drain + 8u;                                                     // epilogue warps
   int* tail = reinterpret_cast<int*>(gen + kGuBarOff + 8 * (kBars + 2));
@@ -870,10 +875,10 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      tc_bar_init(full(s), LDG ? 2 * kGuLoadWarps : 1);
+      tc_bar_init(full(s), ANY ? 2 * kGuLoadWarps : 1);
       tc_bar_init(empty(s), 1);
     }
-    if constexpr (LDG)
+    if constexpr (ANY)
       for (int s = 0; s < kGuRaws; ++s) {
         tc_bar_init(raw_full(s), 1);
         tc_bar_init(raw_empty(s), kGuLoadWarps);
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
     }
     for (int s = 0; s < kGuItems; ++s) {
       tc_bar_init(it_full(s), 1);
-      tc_bar_init(it_empty(s), (LDG ? 1 + kGuLoadWarps : 1) + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
+      tc_bar_init(it_empty(s), (ANY ? 1 + kGuLoadWarps : 1) + (leader ? 1 : 0) + (SCALE_RING ? 1 : 0) + EW);
     }
     tc_bar_init(drain, 1);
     tc_bar_init(join, EW);
@@ -913,7 +918,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
   // experts it takes the whole block (256 experts: 2.9 us, one warp 6.9).
   int whole = 0, halves = 0, n_tiles = -1;
   const bool by_block = OP == G_DW || MT > 1 || g.E > 64;
-  if (by_block) n_tiles = gu_plan<OP, Tiles, gu_threads(LDG)>(g, line, tid, cols, p.split_most, &whole, &halves);
+  if (by_block) n_tiles = gu_plan<OP, Tiles, gu_threads(ANY)>(g, line, tid, cols, p.split_most, &whole, &halves);
   tc_fence_before();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if constexpr (OP != G_DW)
@@ -953,13 +958,13 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
 
   if (warp < 4) {
     // the epilogue gets registers of these warps (the host checks that the block has kGuRegs per thread)
-    if constexpr (LDG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLow));
+    if constexpr (ANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuAnyLow));
     else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
-    if (LDG && warp == 0) {
-      if constexpr (LDG) {
+    if (ANY && warp == 0) {
+      if constexpr (ANY) {
         // ================= TMA issuer of the aligned blocks: lanes 0 .. R - 1
         // the rows of A by their number modulo R, lanes 16 .. 16 + R - 1 those of B
-        constexpr int R = GuLdgParams<FP8>::R;
+        constexpr int R = GuAnyParams<FP8>::R;
         const int c = lane & 15;
         const bool is_b = lane >= 16, mine = c < R;
         const bool mn = is_b ? B_MN : A_MN;
@@ -1271,20 +1276,20 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
       }
       __syncwarp();
     }
-  } else if (LDG && warp >= 4 + kGuEpiWarps) {
-    if constexpr (LDG) {
+  } else if (ANY && warp >= 4 + kGuEpiWarps) {
+    if constexpr (ANY) {
       // ================= the operands' pieces out of the aligned blocks: eight
       // neighbouring lanes have one row's 128 bytes (which hit different banks,
       // read and written); M- or N-major: of 64 rows, each of two panels.
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuLdgLoad));
-      constexpr int ES = FP8 ? 1 : 2, R = GuLdgParams<FP8>::R;
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuAnyLoad));
+      constexpr int ES = FP8 ? 1 : 2, R = GuAnyParams<FP8>::R;
       const int lw = warp - 4 - kGuEpiWarps;  // 0 .. 7
       // rows from number `first` on, of which the first is at `low` modulo 16 bytes
       auto cut = [&](auto mn, uint32_t to, uint32_t from, uint32_t low, uint32_t ld, int first, int rows, uint32_t cls) {
         constexpr bool MN = decltype(mn)::value;
         constexpr int C = MN ? 16 : 8, PITCH = MN ? 272 : 144, J = 32 / C;  // pieces of a row, rows at a time
         const int c = lane & (C - 1);
-#pragma unroll 2
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = (16 / (C / 8)) * lw + lane / C + J * j;
           if (!MN && r - lane / C >= rows) break;
@@ -1334,7 +1339,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
       }
     }
   } else {
-    if constexpr (LDG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuLdgHigh));
+    if constexpr (ANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuAnyHigh));
     else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every H-th 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
@@ -1443,7 +1448,7 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
         if (lane == 0) cl_arrive(cl_addr(acc_empty(seg & (kGuSegs - 1)), 0));
       };
       if constexpr (CHAIN == 0) {
-        if (!LDG && all) {
+        if (!ANY && all) {
           // Rounded to the output's 16 bits on the way into registers, both
           // halves, so that the accumulators are free before the first store:
           // the next tile's MMAs wait for 800 clocks of TMEM reads then, and
@@ -1734,16 +1739,16 @@ __global__ void __launch_bounds__(gu_threads(LDG), 1) grouped_umma_kernel(
 // One translation unit per kernel: gu_launch starts `pairs` clusters, gu_pairs
 // sets the kernel's attributes on the current device and returns how many
 // pairs fit at once (0: none).
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 bool gu_launch(const GuParams& p, int pairs, cudaStream_t s);
-template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool LDG>
+template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 int gu_pairs();
 constexpr int kGuChain = 8;  // 16-bit products with fp32 outputs: 512 contracted values per chain
-#define MOE_GU_DECL(OP, FP8, ROWM, MT, CHAIN, LDG)                                             \
+#define MOE_GU_DECL(OP, FP8, ROWM, MT, CHAIN, ANY)                                             \
   template <>                                                                                  \
-  bool gu_launch<OP, FP8, ROWM, MT, CHAIN, LDG>(const GuParams& p, int pairs, cudaStream_t s); \
+  bool gu_launch<OP, FP8, ROWM, MT, CHAIN, ANY>(const GuParams& p, int pairs, cudaStream_t s); \
   template <>                                                                                  \
-  int gu_pairs<OP, FP8, ROWM, MT, CHAIN, LDG>();
+  int gu_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>();
 MOE_GU_DECL(G_MM, false, false, 1, 0, false)
 MOE_GU_DECL(G_MM, false, false, 2, 0, false)
 MOE_GU_DECL(G_MM, false, false, 1, kGuChain, false)

@@ -4,5 +4,5 @@
 #define GU_ROWM false
 #define GU_MT 1
 #define GU_CHAIN 0
-#define GU_LDG false
+#define GU_ANY false
 #include "gu_inst.inl"

@@ -1,16 +1,16 @@
 // Instantiation unit of the grouped tensor-memory kernel (GU_OP, GU_FP8,
-// GU_ROWM, GU_MT, GU_CHAIN, GU_LDG set by the including file).
+// GU_ROWM, GU_MT, GU_CHAIN, GU_ANY set by the including file).
 #include "grouped_umma.cuh"
 
 namespace moe {
 
 namespace {
-const auto gu_kernel = grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>;
+const auto gu_kernel = grouped_umma_kernel<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_ANY>;
 
 cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(gu_threads(GU_LDG));
+  cfg.blockDim = dim3(gu_threads(GU_ANY));
   cfg.dynamicSmemBytes = gu_smem();
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -26,22 +26,22 @@ cudaLaunchConfig_t gu_config(int pairs, cudaStream_t s, cudaLaunchAttribute* att
 }  // namespace
 
 template <>
-bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>(const GuParams& p, int pairs, cudaStream_t s) {
+bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_ANY>(const GuParams& p, int pairs, cudaStream_t s) {
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gu_config(pairs, s, attr);
-  return cudaLaunchKernelEx(&cfg, gu_kernel, static_cast<const GuKernelParams<GU_FP8, GU_LDG>&>(p)) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, gu_kernel, static_cast<const GuKernelParams<GU_FP8, GU_ANY>&>(p)) == cudaSuccess;
 }
 
 template <>
-int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_LDG>() {
+int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_ANY>() {
   if (cudaFuncSetAttribute(gu_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gu_smem()) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   // the register hand-over of these kernels counts on what the block starts with
   cudaFuncAttributes fa;
-  if (GU_LDG || gu_hand_over(GU_MT, GU_CHAIN)) {
-    if (cudaFuncGetAttributes(&fa, gu_kernel) != cudaSuccess || (fa.numRegs + 7) / 8 * 8 != gu_launch_regs(GU_LDG)) {
+  if (GU_ANY || gu_hand_over(GU_MT, GU_CHAIN)) {
+    if (cudaFuncGetAttributes(&fa, gu_kernel) != cudaSuccess || (fa.numRegs + 7) / 8 * 8 != gu_launch_regs(GU_ANY)) {
       cudaGetLastError();
       return 0;
     }
