@@ -708,8 +708,14 @@ MOE_DEV void gu_rows_out(void* out, int type, long long base, long long ld, int 
             tc_lds128(buf + (uint32_t)(r * 128 + v * 4));
   } else if (lane < vals) {
 #pragma unroll 1
-    for (int r = 0; r < rows; ++r)
-      gmm_store(out, type, base + r * ld + lane, __uint_as_float(tc_lds32(buf + (uint32_t)(r * 128 + lane * 4))));
+    for (int r = 0; r < rows; r += 4) {
+      float t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = __uint_as_float(tc_lds32(buf + (uint32_t)((r + k) * 128 + lane * 4)));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r + k < rows) gmm_store(out, type, base + (r + k) * ld + lane, t[k]);
+    }
   }
   __syncwarp();
 }
@@ -778,12 +784,27 @@ MOE_DEV void gu_lines_out(void* out, long long base, long long ld, int left, int
 #pragma unroll 1
           for (int k = 0; k < n; ++k) value(to + k * ES, from + k * ES);
       }
-    } else {  // rows at any element: 32 neighbouring values per store
+    } else {  // rows at any element: 32 neighbouring values per store, eight on their way
+      constexpr int VS = LB / ES / 32, RS = 8 / VS;
 #pragma unroll 1
-      for (int r = 0; r < rows; ++r)
-#pragma unroll 1
-        for (int v = lane; v < min(left, LB / ES); v += 32)
-          value(o + ((r0 + r) * ld + v) * ES, place(r, v * ES >> 4) + (uint32_t)(v * ES & 15));
+      for (int r = 0; r < rows; r += RS) {
+        uint32_t t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int v = lane + 32 * (k % VS);
+          const uint32_t from = place(r + k / VS, v * ES >> 4) + (uint32_t)(v * ES & 15);
+          t[k] = F32 ? tc_lds32(from) : um_lds16(from);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int v = lane + 32 * (k % VS);
+          char* to = o + ((r0 + r + k / VS) * ld + v) * ES;
+          if (r + k / VS < rows && v < left) {
+            if (F32) *reinterpret_cast<uint32_t*>(to) = t[k];
+            else *reinterpret_cast<uint16_t*>(to) = (uint16_t)t[k];
+          }
+        }
+      }
     }
   }
   __syncwarp();
