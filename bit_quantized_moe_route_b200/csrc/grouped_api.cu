@@ -162,7 +162,8 @@ moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s
       GMM_TRY(classes(q.b_rows, p.x, p.rows, p.n_in, p.ld_x, 272, 64));
     } else {
       const int cols = OP == G_MM ? p.n_in : p.n_out;
-      GMM_TRY(classes(q.a_rows, p.w, (long long)p.E * p.n_out, p.n_in, p.n_in, OP == G_DX ? 272 : 144, OP == G_DX ? 64 : 128));
+      const bool mn = OP == G_DX;
+      GMM_TRY(classes(q.a_rows, p.w, (long long)p.E * p.n_out, p.n_in, p.n_in, mn ? 272 : 144, mn ? 64 : 128));
       if (p.rows > 64) GMM_TRY(classes(q.b_rows, p.rows_in, p.rows, cols, p.ld_rows, 144, 128));
       GMM_TRY(classes(q.b_few, p.rows_in, p.rows, cols, p.ld_rows, 144, 32));
     }

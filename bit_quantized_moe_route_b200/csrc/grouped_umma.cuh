@@ -124,7 +124,8 @@ constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
 constexpr int kGuLoadWarps = 8;
 constexpr int gu_threads(bool any) { return kGuThreads + (any ? 32 * kGuLoadWarps : 0); }
 constexpr int kGuAnyRegs = 96, kGuAnyLow = 64, kGuAnyLoad = 64, kGuAnyHigh = 144;
-static_assert(128 * kGuAnyLow + 32 * kGuLoadWarps * kGuAnyLoad + 32 * kGuEpiWarps * kGuAnyHigh <= gu_threads(true) * kGuAnyRegs,
+static_assert(128 * kGuAnyLow + 32 * kGuLoadWarps * kGuAnyLoad + 32 * kGuEpiWarps * kGuAnyHigh <=
+                  gu_threads(true) * kGuAnyRegs,
               "registers of the block");
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
@@ -997,7 +998,7 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
           if (OP == G_DW && it.kind == GU_ZEROS) continue;
           const int half = it.np >> 1, m = it.m0 + (int)rank * 128, n = it.n0 + (int)rank * half;
           const bool few = !B_MN && half <= 32;
-          const CUtensorMap* map = is_b ? (few ? &p.b_few[c & (R - 1)] : &p.b_rows[c & (R - 1)]) : &p.a_rows[c & (R - 1)];
+          const CUtensorMap* map = (!is_b ? p.a_rows : few ? p.b_few : p.b_rows) + (c & (R - 1));
           // the first step's first row (of the whole operand) and value
           const int k0 = it.kb0 * KE, we = it.e * g.n_out;
           int row = OP == G_DW ? it.r0 + k0 : is_b ? n : OP == G_DX ? we + k0 : we + m;
@@ -1010,7 +1011,8 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
             if (lane == 0) um_expect_tx(raw_full(st), bytes);
             __syncwarp();
             if (mine)
-              um_tma_2d(base + (uint32_t)(NS * kStep + st * 2 * kGuRaw) + to, map, x, (row - c + R - 1) / R, raw_full(st));
+              um_tma_2d(base + (uint32_t)(NS * kStep + st * 2 * kGuRaw) + to, map, x, (row - c + R - 1) / R,
+                        raw_full(st));
             if (mn) row += 64;
             else x += KE;
             ++issued;
@@ -1334,9 +1336,11 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
         // numbers of the rows as the issuer has them, addresses and row strides modulo 16 bytes
         int a_row = OP == G_DW ? it.r0 + k0 : OP == G_DX ? we + k0 : we + m, b_row = OP == G_DW ? it.r0 + k0 : n;
         int left = OP == G_DW ? it.r1 - it.r0 - k0 : g.n_out - k0;  // contracted rows (M- or N-major)
-        const uint32_t lda = (uint32_t)(OP == G_DW ? g.ld_rows : g.n_in) * ES, ldb = (uint32_t)(OP == G_DW ? g.ld_x : g.ld_rows) * ES;
-        const uint32_t a_low = (uint32_t)reinterpret_cast<uintptr_t>(OP == G_DW ? g.rows_in : g.w) + (uint32_t)a_row * lda;
-        const uint32_t b_low = (uint32_t)reinterpret_cast<uintptr_t>(OP == G_DW ? g.x : g.rows_in) + (uint32_t)b_row * ldb;
+        const uint32_t lda = (uint32_t)(OP == G_DW ? g.ld_rows : g.n_in) * ES;
+        const uint32_t ldb = (uint32_t)(OP == G_DW ? g.ld_x : g.ld_rows) * ES;
+        const void *a_at = OP == G_DW ? g.rows_in : g.w, *b_at = OP == G_DW ? g.x : g.rows_in;
+        const uint32_t a_low = (uint32_t)reinterpret_cast<uintptr_t>(a_at) + (uint32_t)a_row * lda;
+        const uint32_t b_low = (uint32_t)reinterpret_cast<uintptr_t>(b_at) + (uint32_t)b_row * ldb;
         const uint32_t a_cls = gu_raw_class<FP8>(A_MN, false), b_cls = gu_raw_class<FP8>(B_MN, few);
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           ok = __all_sync(0xffffffffu, cl_bar_wait(raw_full(rs), rph, abort_flag) &&

@@ -374,9 +374,10 @@ size_t moe_grouped_workspace_size(void);
  *   y  : [rows, n_out] (out), ld_y >= n_out; overlaps no input
  *        (column ranges of one buffer with one row stride may lie side by side)
  * Pointers are aligned to their elements.  Operands whose base address, row
- * stride and (weights) row length are multiples of 16 bytes are copied by TMA;
- * others come through registers, more slowly (about a fifth of the rate of
- * large products), with the same results up to the order of the fp32 sums.
+ * stride and (weights) row length are multiples of 16 bytes are copied as they
+ * are; if any is not, both are brought in aligned blocks and cut to size, more
+ * slowly (about 0.4 of the rate of large products), with the same results up to
+ * the order of the fp32 sums.
  * Results do not depend on what else runs: the same call gives the same bits.
  */
 moe_status_t moe_grouped_mm(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const void* w,
