@@ -656,3 +656,90 @@ def test_any_alignment_items(cuda_device, ws, op, n_in, n_out):
 def test_fp8_any_alignment_items(cuda_device, ws, n_in, n_out):
     for shift, ld_pad in ((0, 0), (1, 0), (9, 5)):
         run_fp8([1, 0, 0, 0, 0, 0, 2, 0, 200, 0, 1, 70], n_in, n_out, BF, cuda_device, ws, ld_pad=ld_pad, shift=shift, pad=2)
+
+
+@pytest.mark.parametrize("n_in,pitch", [(128, 32776), (129, 32771)])
+def test_rows_beyond_4_gib(cuda_device, ws, n_in, pitch):
+    """Rows whose byte offsets pass 32 bits, in and out."""
+    rows, n_out, dev = 70000, 40, cuda_device
+    g = gen(3, dev)
+    x = torch.empty(rows * pitch, dtype=BF, device=dev).view(rows, pitch)[:, 5 if n_in == 129 else 8:][:, :n_in]
+    x.copy_(normal(g, BF, rows, n_in))
+    y = torch.empty(rows * pitch, dtype=BF, device=dev).view(rows, pitch)[:, :n_out]
+    off = offsets_of([rows - 300, 0, 300], dev)
+    w, dy = normal(g, BF, 3, n_out, n_in, std=0.05), normal(g, BF, rows, n_out)
+    moe.grouped_mm(x, w, off, y, ws)
+    dw = torch.empty(3, n_out, n_in, dtype=FP, device=dev)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    dx = y.as_strided((rows, n_in), (pitch, 1), 64)
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    ref, mag = reference("mm", x, w, off, 3)
+    close(y, ref, mag, n_in)
+    ref, mag = reference("dx", dy, w, off, 3)
+    close(dx, ref, mag, n_out)
+    ref, mag = reference("dw", dy, x, off, 3)
+    close(dw, ref, mag, torch.tensor([rows - 300, 0, 300], device=dev)[:, None, None])
+
+
+@pytest.mark.parametrize("n_in", [8192, 8191])
+def test_weights_beyond_4_gib(cuda_device, ws, n_in):
+    """Matrices whose byte offsets pass 32 bits: read by the products, written by their gradient."""
+    E, n_out, dev = 40, 8192, cuda_device
+    g = gen(4, dev)
+    counts = [2] + [0] * (E - 2) + [3]
+    off = offsets_of(counts, dev)
+    w = torch.empty(E, n_out, n_in, dtype=BF, device=dev)
+    w[0], w[E - 1] = normal(g, BF, n_out, n_in, std=0.05), normal(g, BF, n_out, n_in, std=0.05)
+    x, dy = normal(g, BF, 5, n_in), normal(g, BF, 5, n_out)
+    y, dx = torch.empty_like(dy), torch.empty_like(x)
+    moe.grouped_mm(x, w, off, y, ws)
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    for lo, hi, e in ((0, 2, 0), (2, 5, E - 1)):
+        m = w[e].double()
+        close(y[lo:hi], x[lo:hi].double() @ m.t(), x[lo:hi].double().abs() @ m.t().abs(), n_in)
+        close(dx[lo:hi], dy[lo:hi].double() @ m, dy[lo:hi].double().abs() @ m.abs(), n_out)
+    moe.grouped_mm_dw(dy, x, off, w, ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    assert not bool(w[1:E - 1].any())
+    for lo, hi, e in ((0, 2, 0), (2, 5, E - 1)):
+        u, v = dy[lo:hi].double(), x[lo:hi].double()
+        close(w[e], u.t() @ v, u.abs().t() @ v.abs(), hi - lo)
+
+
+@pytest.mark.parametrize("n_in", [136, 137])
+def test_replays_on_another_stream(cuda_device, n_in):
+    """A captured forward and both gradients, replayed beside an eager call with a workspace of its own."""
+    dev, g = cuda_device, gen(9, cuda_device)
+    counts, n_out = [3, 0, 130, 1, 40], 200
+    off, rows = offsets_of(counts, dev), sum(counts)
+    x, dy, w = normal(g, BF, rows, n_in), normal(g, BF, rows, n_out), normal(g, BF, 5, n_out, n_in, std=0.05)
+
+    def run(ws, y, dx, dw):
+        moe.grouped_mm(x, w, off, y, ws)
+        moe.grouped_mm_dx(dy, w, off, dx, ws)
+        moe.grouped_mm_dw(dy, x, off, dw, ws)
+
+    def outs():
+        return torch.zeros_like(dy), torch.zeros_like(x), torch.zeros_like(w)
+
+    ws1, ws2 = moe.alloc_grouped_workspace(dev), moe.alloc_grouped_workspace(dev)
+    want, got, other = outs(), outs(), outs()
+    run(ws2, *want)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(ws1, *got)
+    for _ in range(4):
+        for t in got + other:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            run(ws2, *other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, other))
