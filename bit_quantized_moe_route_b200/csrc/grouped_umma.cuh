@@ -15,9 +15,10 @@
 //   mm, ROWM    x rows, K-major            W[e] rows o, K-major
 //
 // With the rows on the M side (ROWM: dw, whose output rows are o, and the 8-bit
-// product of many rows per expert) a thread has one output row, so it stores
-// from its registers and has one row scale; with them on the N side the M side
-// is the output's contiguous dimension.
+// product of many rows per expert) a thread has one output row and one row
+// scale; with them on the N side the M side is the output's contiguous
+// dimension.  Either way the output leaves through shared memory, in whole
+// lines (the 8-bit product of aligned rows: from the registers).
 //
 // MT = 2 (16-bit products with enough tiles): a tile is 512 values of the M
 // side, two MMAs of 256 that share the B operand.  Per product that moves three
@@ -554,10 +555,12 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   // evenly, for at most as many pairs as there are, or all of it is the line,
   // whichever costs less.  Measured, in us, for tiles of np columns: a step
   // 0.145 + np / 3000 (8-bit of over 64 columns, which hand over every other
-  // step: 0.45; ANY: 0.45 + np / 470); joining k parts 0.4 + np / 62 + k (0.2 + np / 154).  E.g. 128
-  // steps of 32 columns: whole 33.0, in four 18.2, eight 17.2, sixteen 20.1; 19
-  // steps of 240: whole 13.6, in two 20.7.  dw, whose tiles differ in length:
-  // dealt if the longest are short, else the line.
+  // step: 0.45; ANY: 0.45 + np / 470); joining k parts 0.4 + np / 62 + k (0.2 +
+  // np / 154).  E.g. 128 steps of 32 columns: whole 33.0, in four 18.2, eight
+  // 17.2, sixteen 20.1; 19 steps of 240: whole 13.6, in two 20.7.  dw, whose
+  // tiles differ in length:
+  // dealt if the longest have at most 40 steps (256 rows over ten experts: 179 us,
+  // on the line 265), else the line.
   int halves = 0, each_in = 0;
   {
     const int q = rest / cols, r = rest - q * cols;
@@ -572,7 +575,7 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
       // columns of a tile, on average
       const float np = Tiles::kRowsM ? (float)min(kGuN, p.n_out)
                                      : fminf((float)kGuN, (float)rows * m_tiles / max(1, n_tiles) + 8.f);
-      const float step = Tiles::kAny                 ? 0.45f + np * (1.f / 470.f)
+      const float step = Tiles::kAny                ? 0.45f + np * (1.f / 470.f)
                          : Tiles::kFp8 && np > 64.f ? 0.45f
                                                     : 0.145f + np * (1.f / 3000.f);
       const float join = 0.4f + np * (1.f / 62.f), part = 0.2f + np * (1.f / 154.f);
