@@ -814,26 +814,16 @@ MOE_DEV void gu_lines_out(void* out, long long base, long long ld, int left, int
   __syncwarp();
 }
 
-// Zeros to `vals` rows of `cols` (at most 128) values of es bytes.
-MOE_DEV void gu_zeros_out(char* o, long long ld, int cols, int vals, int es, int unit) {
+// This warp's share, the part-th of `parts`, of `bytes` zeros.
+MOE_DEV void gu_zeros_out(char* o, int bytes, int part, int parts) {
   const int lane = threadIdx.x & 31;
-  if (unit >= 16) {
-    const int wide = es == 4 ? 32 : 16, c = lane & (wide - 1), left = cols - c * (16 / es);  // 16-byte pieces of a row
-    const int step = 32 / wide;
+  const int head = min(bytes, (int)(-reinterpret_cast<uintptr_t>(o) & 15)), n = (bytes - head) >> 4;
 #pragma unroll 4
-    for (int r = lane / wide; r < vals; r += step) {
-      char* to = o + r * ld + 16 * c;
-      if (left >= 16 / es) *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-      else
-#pragma unroll 1
-        for (int i = 0; i < left * es; i += 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
-    }
-  } else {
-#pragma unroll 1
-    for (int r = 0; r < vals; ++r)
-#pragma unroll 1
-      for (int i = 2 * lane; i < cols * es; i += 64) *reinterpret_cast<uint16_t*>(o + r * ld + i) = 0;
-  }
+  for (int i = 32 * part + lane; i < n; i += 32 * parts)
+    *reinterpret_cast<uint4*>(o + head + 16 * i) = make_uint4(0, 0, 0, 0);
+  if (part == 0 && 2 * lane < head) *reinterpret_cast<uint16_t*>(o + 2 * lane) = 0;
+  const int end = head + 16 * n + 2 * lane;
+  if (part == 1 && end < bytes) *reinterpret_cast<uint16_t*>(o + end) = 0;
 }
 
 // 32 bytes to a 32-byte aligned address: one whole sector per lane and store
@@ -1454,12 +1444,14 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
       };
       if constexpr (OP == G_DW) {
         if (it.kind == GU_ZEROS) {
-          const int cols = min(it.nv, 32 * c_end) - 32 * c_first;
+          // An expert's matrix has no gaps, and all tiles of 256 of its rows
+          // are zeros: each writes its share of those rows as one run, whatever
+          // their alignment.
           for (int half = 0; half < it.halves; ++half) {
-            char* o = reinterpret_cast<char*>(g.out) + (ob + 32 * c_first) * out_bytes;
-            gu_zeros_out(o, ld * out_bytes, cols, vals, out_bytes, unit);
-            ob += 256 * ld;
-            vals = min(32, it.mv - 256 - m);
+            const int mv = min(256, it.mv - 256 * half);
+            char* o = reinterpret_cast<char*>(g.out) +
+                      (((long long)it.e * g.n_out + it.m0 + 256 * half) * g.n_in + (long long)mv * it.n0) * out_bytes;
+            if (mv > 0) gu_zeros_out(o, mv * it.nv * out_bytes, (int)rank * EW + warp - 4, 2 * EW);
           }
           continue;
         }
