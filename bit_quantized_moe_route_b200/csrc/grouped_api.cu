@@ -213,7 +213,8 @@ moe_status_t run_gmm(const GmmProblem& p, int in_type, void* ws, cudaStream_t s)
   if (!tma_ok<OP>(p, fp8 ? 1 : 2)) {
     if constexpr (OP == G_MM)
       if (fp8) return launch_umma<OP, true, false, 1, 1, true>(p, in_type, ws, s);
-    return launch_umma<OP, false, ROWM, 1, 0, true>(p, in_type, ws, s);
+    return p.out_type == G_FP32 ? launch_umma<OP, false, ROWM, 1, kGuChain, true>(p, in_type, ws, s)
+                                : launch_umma<OP, false, ROWM, 1, 0, true>(p, in_type, ws, s);
   }
   if constexpr (OP == G_MM)
     if (fp8)

@@ -70,7 +70,10 @@
 //
 // CHAIN = 0: the tile's whole sum is taken in tensor memory.  CHAIN > 0: every
 // CHAIN steps the sum is handed to the epilogue warps, which add it to sums in
-// registers with ordinary fp32 additions.
+// registers with ordinary fp32 additions.  The tensor core truncates as it adds:
+// for positive operands a sum of 65,536 products taken whole is 1.0e-5 of its
+// size too low and one of 2^20 3.8e-4, chained both are 1.1e-7.  So outputs in
+// fp32 are chained, whatever the operands' alignment.
 //
 // The 8-bit product hands over every step (CHAIN = 1), since its scales change
 // there: register sum += scale[row] * step sum, on pairs of columns (packed
@@ -124,9 +127,19 @@ constexpr bool gu_hand_over(int mt, int chain) { return mt > 1 || chain > 0; }
 // ANY: eight more warps; less for each.
 constexpr int kGuLoadWarps = 8;
 constexpr int gu_threads(bool any) { return kGuThreads + (any ? 32 * kGuLoadWarps : 0); }
-constexpr int kGuAnyRegs = 96, kGuAnyLow = 64, kGuAnyLoad = 64, kGuAnyHigh = 144;
-static_assert(128 * kGuAnyLow + 32 * kGuLoadWarps * kGuAnyLoad + 32 * kGuEpiWarps * kGuAnyHigh <=
-                  gu_threads(true) * kGuAnyRegs,
+constexpr int kGuAnyRegs = 96;
+struct GuAnyShare {  // of warps 0-3, the load warps and the epilogue
+  int low, load, high;
+  constexpr bool fits() const {
+    return 128 * low + 32 * kGuLoadWarps * load + 32 * kGuEpiWarps * high <= gu_threads(true) * kGuAnyRegs;
+  }
+};
+// Chained 16-bit sums are 128 in each thread of the epilogue.  (With 64 of them, tiles half as wide, and the other
+// split: 32,768 rows over 32 experts with 2,047 inputs took 1,476 / 1,501 / 1,524 us, not 921 / 1,023 / 1,098: mm, dx, dw.)
+constexpr GuAnyShare gu_any_share(bool fp8, int chain) {
+  return chain > 0 && !fp8 ? GuAnyShare{48, 48, 168} : GuAnyShare{64, 64, 144};
+}
+static_assert(gu_any_share(true, 1).fits() && gu_any_share(false, 0).fits() && gu_any_share(false, 8).fits(),
               "registers of the block");
 constexpr int kGuRegs = 168, kGuRegsLow = 88, kGuRegsHigh = 208;
 static_assert(128 * kGuRegsLow + (kGuThreads - 128) * kGuRegsHigh <= kGuThreads * kGuRegs, "registers of the block");
@@ -847,7 +860,8 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
   static_assert(!FP8 || CHAIN == 1, "the 8-bit product hands over every step");
   static_assert(MT == 1 || (CHAIN == 0 && !ANY), "register sums and loads hold one MMA's");
   // what the kernel knows of the output's type: 1 fp32, 0 16 bits, -1 nothing
-  constexpr int F32 = FP8 || ANY ? -1 : CHAIN ? 1 : 0;
+  constexpr int F32 = FP8 ? -1 : CHAIN ? 1 : 0;
+  constexpr GuAnyShare kShare = gu_any_share(FP8, CHAIN);  // ANY
   constexpr int NS = ANY ? 2 : 12 / (MT + 1);  // stages
   constexpr int kStep = (MT + 1) * kGuTile;   // bytes of one: A (MT x 128 rows), B
   using Tiles = GuTiles<OP, FP8, ROWM, MT, ANY>;
@@ -976,7 +990,7 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
 
   if (warp < 4) {
     // the epilogue gets registers of these warps (the host checks that the block has kGuRegs per thread)
-    if constexpr (ANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuAnyLow));
+    if constexpr (ANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kShare.low));
     else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuRegsLow));
     if (ANY && warp == 0) {
       if constexpr (ANY) {
@@ -1300,7 +1314,7 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
       // ================= the operands' pieces out of the aligned blocks: eight
       // neighbouring lanes have one row's 128 bytes (which hit different banks,
       // read and written); M- or N-major: of 64 rows, each of two panels.
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGuAnyLoad));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kShare.load));
       constexpr int ES = FP8 ? 1 : 2, R = GuAnyParams<FP8>::R;
       const int lw = warp - 4 - kGuEpiWarps;  // 0 .. 7
       // rows from number `first` on, of which the first is at `low` modulo 16 bytes
@@ -1360,7 +1374,7 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
       }
     }
   } else {
-    if constexpr (ANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuAnyHigh));
+    if constexpr (ANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kShare.high));
     else if constexpr (gu_hand_over(MT, CHAIN)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGuRegsHigh));
     // ================= epilogue: 32 TMEM lanes (M values) and every H-th 32 columns (output rows) per warp
     const int q = warp & 3, h = (warp - 4) >> 2;
@@ -1620,6 +1634,7 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
             ++seg;
           }
         } else {
+          constexpr int LW = ANY ? 16 : 32;  // columns at a time; ANY has no registers for 32 beside the sums
           for (int kb = it.kb0; kb < it.kb1; kb += CHAIN) {
             const int at = ring.take(it.np);
             ok = wait_sums();
@@ -1628,12 +1643,15 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
               if (c_first + C_STEP * j < c_end) {
-                uint32_t r[32];
-                gu_ld_issue(ta + 32u * (c_first + C_STEP * j), r);
-                gu_ld_wait(r);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                  gu_add2(acc[j][i / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                for (int u = 0; u < 32; u += LW) {
+                  uint32_t r[LW];
+                  gu_ld_issue(ta + 32u * (c_first + C_STEP * j) + u, r);
+                  gu_ld_wait(r);
+#pragma unroll
+                  for (int i = 0; i < LW; i += 2)
+                    gu_add2(acc[j][(u + i) / 2], gu_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                }
               }
             give_back();
             ++seg;
@@ -1776,14 +1794,17 @@ MOE_GU_DECL(G_MM, false, false, 1, 0, false)
 MOE_GU_DECL(G_MM, false, false, 2, 0, false)
 MOE_GU_DECL(G_MM, false, false, 1, kGuChain, false)
 MOE_GU_DECL(G_MM, false, false, 1, 0, true)
+MOE_GU_DECL(G_MM, false, false, 1, kGuChain, true)
 MOE_GU_DECL(G_DX, false, false, 1, 0, false)
 MOE_GU_DECL(G_DX, false, false, 2, 0, false)
 MOE_GU_DECL(G_DX, false, false, 1, kGuChain, false)
 MOE_GU_DECL(G_DX, false, false, 1, 0, true)
+MOE_GU_DECL(G_DX, false, false, 1, kGuChain, true)
 MOE_GU_DECL(G_DW, false, true, 1, 0, false)
 MOE_GU_DECL(G_DW, false, true, 2, 0, false)
 MOE_GU_DECL(G_DW, false, true, 1, kGuChain, false)
 MOE_GU_DECL(G_DW, false, true, 1, 0, true)
+MOE_GU_DECL(G_DW, false, true, 1, kGuChain, true)
 MOE_GU_DECL(G_MM, true, false, 1, 1, false)
 MOE_GU_DECL(G_MM, true, true, 1, 1, false)
 MOE_GU_DECL(G_MM, true, false, 1, 1, true)

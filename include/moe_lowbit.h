@@ -378,6 +378,8 @@ size_t moe_grouped_workspace_size(void);
  * are; if any is not, both are brought in aligned blocks and cut to size, more
  * slowly (about 0.4 of the rate of large products), with the same results up to
  * the order of the fp32 sums.
+ * For an fp32 output at most 512 products at a time are added by the tensor
+ * core, which truncates, and those sums by fp32 additions to nearest.
  * Results do not depend on what else runs: the same call gives the same bits.
  */
 moe_status_t moe_grouped_mm(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const void* w,

@@ -743,3 +743,39 @@ def test_replays_on_another_stream(cuda_device, n_in):
             run(ws2, *other)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, other))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_long_fp32_sums_do_not_drift(cuda_device, ws, op, shift):
+    """fp32 outputs of long sums of positive products, operands aligned and not: no drift from an accumulator that
+    truncates.
+
+    Values are 1 + j/16, so products have 8 fractional bits and are below 4: a sum of 512 of them is below 2^11 and
+    has 19 bits, exact however it is taken.  What is left are ordinary additions of such sums, one for each 512
+    products and at most two more for each of up to 74 parts of a tile; each rounds a partial sum, at most the whole,
+    to nearest: 2^-24 of it.  Taken in one truncating accumulator the same sums are several times as far off."""
+    length, m, n = 65536, 2560, 2048
+    g = gen(17 + shift, cuda_device)
+
+    def values(*shape):
+        count = int(np.prod(shape))
+        v = torch.randint(0, 16, (count + shift,), generator=g, device=cuda_device).to(BF) / 16 + 1
+        return v[shift:].view(shape)
+
+    if op == "mm":
+        x, w, y = values(m, length), values(1, n, length), torch.empty(m, n, dtype=FP, device=cuda_device)
+        moe.grouped_mm(x, w, None, y, ws)
+        ref = x.double() @ w[0].double().t()
+    elif op == "dx":
+        dy, w, y = values(m, length), values(1, length, n), torch.empty(m, n, dtype=FP, device=cuda_device)
+        moe.grouped_mm_dx(dy, w, None, y, ws)
+        ref = dy.double() @ w[0].double()
+    else:
+        dy, x, y = values(length, m), values(length, n), torch.empty(1, m, n, dtype=FP, device=cuda_device)
+        moe.grouped_mm_dw(dy, x, None, y, ws)
+        ref = (dy.double().t() @ x.double())[None]
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == 0
+    err = ((y.double() - ref).abs() / ref).max().item()
+    assert err <= (length / 512 + 2 * 74) * 2.0 ** -24, err
