@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -43,12 +44,46 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in inputs())
 
 
+def launch_registers(src: str):
+    """Registers per thread that the grouped kernel of `src` counts on when it starts (its warps share them out), or
+    None: another source, or a kernel that leaves them as they are."""
+    if not os.path.basename(src).startswith("gu_"):
+        return None
+    with open(src) as f:
+        form = dict(re.findall(r"#define GU_(\w+) (\w+)", f.read()))
+    with open(os.path.join(CSRC, "grouped_umma.cuh")) as f:
+        regs = dict(re.findall(r"\b(kGuRegs|kGuAnyRegs) = (\d+)", f.read()))
+    if form["ANY"] == "true":
+        return int(regs["kGuAnyRegs"])
+    return int(regs["kGuRegs"]) if form["MT"] != "1" or form["CHAIN"] != "0" else None
+
+
+def check_registers(src: str, ptxas_log: str) -> None:
+    """Raise unless ptxas gave the one kernel of `src` the registers it counts on (in the launch's units of 8)."""
+    want = launch_registers(src)
+    if want is None:
+        return
+    used = [int(n) for n in re.findall(r"Used (\d+) registers", ptxas_log)]
+    if [-(-n // 8) * 8 for n in used] != [want]:
+        raise RuntimeError(f"{os.path.basename(src)}: compiled to {used} registers, its warps share out {want} each")
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-    cmd = [nvcc(), *ARCH, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src]
+    cmd = [nvcc(), *ARCH, *FLAGS, "-Xptxas", "-v", "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src]
     if verbose:
         print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    run = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if run.returncode:
+        raise RuntimeError(f"nvcc failed on {src}:\n{run.stdout}")
+    for line in run.stdout.splitlines():
+        if "warning" in line:
+            print(line, flush=True)
+    try:
+        check_registers(src, run.stdout)
+    except RuntimeError:
+        os.remove(obj)
+        raise
     return obj
 
 

@@ -3,9 +3,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "api_util.h"
+#include "device_cache.h"
 #include "grouped_umma.cuh"
 #include "quant_fp8.cuh"
 
@@ -22,16 +22,14 @@ constexpr size_t kGmmWsBytes = kGuWsBytes;
   } while (0)
 
 int sm_count(int* sms) {
-  static std::atomic<int> cached[64];
+  static DeviceCache cached;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  int v = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
-  if (!v) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    if (dev < 64) cached[dev].store(v, std::memory_order_relaxed);
-  }
-  *sms = v;
-  return 0;
+  *sms = cached.get(dev, [dev] {
+    int v = 0;
+    return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 0;
+  });
+  return *sms < 1;
 }
 
 size_t type_bytes(int t) { return t == G_FP32 ? 4 : t == G_E4M3 ? 1 : 2; }
@@ -102,18 +100,13 @@ moe_status_t check_gmm_ws(void* ws, size_t ws_bytes) {
   return api_check_dev_ptr(ws, "workspace");
 }
 
-// Resident pairs of a tensor-memory kernel on the current device (0: none).
+// Resident pairs of a tensor-memory kernel on the current device, or a GuNoPairs.
 template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 int resident_pairs() {
-  static std::atomic<int> cached[64];  // pairs + 1
+  static DeviceCache cached;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int v = cached[dev].load(std::memory_order_acquire);
-  if (!v) {
-    v = gu_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>() + 1;
-    cached[dev].store(v, std::memory_order_release);
-  }
-  return v - 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GU_QUERY_FAILED;
+  return cached.get(dev, gu_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>);
 }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
@@ -131,6 +124,10 @@ constexpr long long kRowsPerExpertM = 192;
 template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 moe_status_t launch_umma(const GmmProblem& p, int type, void* ws, cudaStream_t s) {
   const int pairs = resident_pairs<OP, FP8, ROWM, MT, CHAIN, ANY>();
+  if (pairs == GU_QUERY_FAILED)
+    return api_fail(MOE_ERR_CUDA, "grouped_umma_kernel: %s", cudaGetErrorString(cudaGetLastError()));
+  if (pairs == GU_REGISTERS)
+    return api_fail(MOE_ERR_CUDA, "the grouped kernel was not compiled to the registers that its warps share out");
   if (pairs < 1) return api_fail(MOE_ERR_CUDA, "the grouped kernel does not fit this device");
   GuKernelParams<FP8, ANY> q;
   q.g = p;

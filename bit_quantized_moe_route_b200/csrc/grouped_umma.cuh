@@ -1779,7 +1779,9 @@ __global__ void __launch_bounds__(gu_threads(ANY), 1) grouped_umma_kernel(
 
 // One translation unit per kernel: gu_launch starts `pairs` clusters, gu_pairs
 // sets the kernel's attributes on the current device and returns how many
-// pairs fit at once (0: none).
+// pairs fit at once, or why it cannot tell (GU_QUERY_FAILED: the runtime's last
+// error says).
+enum GuNoPairs : int { GU_NO_FIT = 0, GU_QUERY_FAILED = -1, GU_REGISTERS = -2 };
 template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>
 bool gu_launch(const GuParams& p, int pairs, cudaStream_t s);
 template <int OP, bool FP8, bool ROWM, int MT, int CHAIN, bool ANY>

@@ -34,25 +34,19 @@ bool gu_launch<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_ANY>(const GuParams& 
 
 template <>
 int gu_pairs<GU_OP, GU_FP8, GU_ROWM, GU_MT, GU_CHAIN, GU_ANY>() {
-  if (cudaFuncSetAttribute(gu_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gu_smem()) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  // the register hand-over of these kernels counts on what the block starts with
+  if (cudaFuncSetAttribute(gu_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gu_smem()) != cudaSuccess)
+    return GU_QUERY_FAILED;
+  // The register hand-over of these kernels counts on what the block starts
+  // with: with fewer its epilogue would wait for ever (the build checks it too).
   cudaFuncAttributes fa;
   if (GU_ANY || gu_hand_over(GU_MT, GU_CHAIN)) {
-    if (cudaFuncGetAttributes(&fa, gu_kernel) != cudaSuccess || (fa.numRegs + 7) / 8 * 8 != gu_launch_regs(GU_ANY)) {
-      cudaGetLastError();
-      return 0;
-    }
+    if (cudaFuncGetAttributes(&fa, gu_kernel) != cudaSuccess) return GU_QUERY_FAILED;
+    if ((fa.numRegs + 7) / 8 * 8 != gu_launch_regs(GU_ANY)) return GU_REGISTERS;
   }
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gu_config(1, nullptr, attr);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gu_kernel, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
+  if (cudaOccupancyMaxActiveClusters(&n, gu_kernel, &cfg) != cudaSuccess) return GU_QUERY_FAILED;
   return n < kGuPairsMax ? n : kGuPairsMax;
 }
 
