@@ -392,7 +392,8 @@ def grouped_mm_fp8(x, x_scales, w, w_scales, expert_offsets, y, ws, stream=None)
 
     x [R, n_in] and x_scales float32 [ceil(n_in/128), R] as quant_fp8 writes
     them; w [E, n_out, n_in] and w_scales float32 [E, ceil(n_out/128),
-    ceil(n_in/128)].  Codes are float8_e4m3fn or uint8 tensors.
+    ceil(n_in/128)].  Codes are float8_e4m3fn or uint8 tensors.  The product
+    of a group's two scales is to be zero or a normal fp32 number.
     expert_offsets None with E = 1: one matrix for every row.  y bfloat16,
     float16 or float32 [R, n_out]."""
     if w.dim() != 3 or w.dtype not in _FP8_TYPES or x.dtype not in _FP8_TYPES:

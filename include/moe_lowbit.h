@@ -415,8 +415,11 @@ moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64
  *   w        : e4m3 [n_experts, n_out, n_in]
  *   w_scales : fp32 [n_experts, ceil(n_out/128), ceil(n_in/128)] (e8m0 block
  *              scales of a checkpoint widen to fp32 exactly)
- * The sums of a group are taken over exact products; scales may be any fp32
- * values.  Otherwise as moe_grouped_mm.
+ * The sums of a group are taken over exact products.  Its two scales are
+ * multiplied with each other first, in fp32: of any size and sign themselves,
+ * their product is to be zero or a normal number.  (A product that is
+ * subnormal moves an output by up to 2^-125; one beyond fp32 makes it infinite
+ * or NaN, for a sum of zero too.)  Otherwise as moe_grouped_mm.
  */
 moe_status_t moe_grouped_mm_fp8(const moe_gmm_dims_t* dims, const void* x, int64_t ld_x, const float* x_scales,
                                 const void* w, const float* w_scales, const int32_t* expert_offsets, void* y,

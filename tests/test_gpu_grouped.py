@@ -779,3 +779,39 @@ def test_long_fp32_sums_do_not_drift(cuda_device, ws, op, shift):
     assert moe.read_device_error(ws) == 0
     err = ((y.double() - ref).abs() / ref).max().item()
     assert err <= (length / 512 + 2 * 74) * 2.0 ** -24, err
+
+
+@pytest.mark.parametrize("counts,n_in", [([40, 3], 384), ([300, 500], 384), ([40, 3], 383)])
+@pytest.mark.parametrize("a,b", [(-63, -63), (-126, 0), (100, -120), (127, -60), (60, 36), (-3, 99)])
+def test_fp8_scales_of_any_size(cuda_device, ws, counts, n_in, a, b):
+    """Scales near both ends of fp32 whose product is normal, one sign or the other, zeros and zero blocks among them."""
+    g, rows, n_out, dev = gen(a + 2 * b + 500, cuda_device), sum(counts), 136, cuda_device
+    codes, sx, w, sw = fp8_inputs(g, 2, rows, n_in, n_out)
+    sx = torch.full_like(sx, 2.0 ** a) * (1 - 2.0 * (torch.arange(rows, device=dev) % 2))
+    sw = torch.full_like(sw, 2.0 ** b)
+    sx[1, ::3], sw[1, 0, 2] = 0.0, 0.0
+    codes[5:9, :128] = 0
+    sx[0, 5:9] = min(2.0 ** (127 - max(b, 0)), 2.0 ** 127)        # the largest for this b: the blocks are zero
+    y = torch.zeros(rows, n_out, dtype=FP, device=dev)
+    moe.grouped_mm_fp8(codes, sx, w, sw, offsets_of(counts, dev), y, ws)
+    assert moe.read_device_error(ws) == 0 and bool(torch.isfinite(y).all())
+    ref, mag = reference("mm", fp8_wide(codes, sx), fp8_wide(w, sw), offsets_of(counts, dev), 2)
+    close(y, ref, mag, n_in)
+
+
+@pytest.mark.parametrize("counts,n_in", [([40, 3], 384), ([300, 500], 384), ([40, 3], 383)])
+def test_fp8_scales_with_a_subnormal_product(cuda_device, ws, counts, n_in):
+    """The product is rounded to a multiple of 2^-149, off by 2^-150 at most; times a group's sum, at most
+    128 * 448 * 448 < 2^24.7, that is 2^-125.3 a group.  The quantiser's scale of a block of zeros gives exact zeros."""
+    g, rows, n_out, dev = gen(77, cuda_device), sum(counts), 136, cuda_device
+    codes, sx, w, sw = fp8_inputs(g, 2, rows, n_in, n_out)
+    sx, sw = torch.full_like(sx, 1.7 * 2.0 ** -70), torch.full_like(sw, 1.9 * 2.0 ** -71)
+    codes[:, :128], sx[0], sw[:, :, 0] = 0, 2.0 ** -126, 0.3       # blocks of zeros
+    y = torch.zeros(rows, n_out, dtype=FP, device=dev)
+    off = offsets_of(counts, dev)
+    moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
+    ref, mag = reference("mm", fp8_wide(codes, sx), fp8_wide(w, sw), off, 2)
+    assert bool(((y.double() - ref).abs() <= 2 * 2.0 ** -125.3 + (n_in + 4) * 2.0 ** -23 * mag).all())
+    codes.zero_()
+    moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
+    assert bool((y == 0).all()) and moe.read_device_error(ws) == 0
