@@ -253,8 +253,9 @@ moe_status_t rows_product(const moe_gmm_dims_t* d, const char* in_name, const vo
   GMM_TRY(check_aligned(ins[4], 4));
   GMM_TRY(check_aligned(o, type_bytes(d->out_dtype)));
   GMM_TRY(check_apart(o, ins, 5));
-  const Span wsp = flat_span("ws", ws, ws_bytes);
+  const Span wsp = flat_span("ws", ws, kGmmWsBytes);
   GMM_TRY(check_apart(o, &wsp, 1));
+  GMM_TRY(check_apart(wsp, ins, 5));
   GmmProblem p{};
   p.w = w;
   p.rows_in = in;
@@ -313,8 +314,9 @@ moe_status_t moe_grouped_mm_dw(const moe_gmm_dims_t* dims, const void* dy, int64
   GMM_TRY(check_aligned(ins[2], 4));
   GMM_TRY(check_aligned(o, type_bytes(d.out_dtype)));
   GMM_TRY(check_apart(o, ins, 3));
-  const Span wsp = flat_span("ws", ws, ws_bytes);
+  const Span wsp = flat_span("ws", ws, kGmmWsBytes);
   GMM_TRY(check_apart(o, &wsp, 1));
+  GMM_TRY(check_apart(wsp, ins, 3));
   GmmProblem p{};
   p.rows_in = dy;
   p.x = x;

@@ -358,8 +358,9 @@ typedef struct {
  * dims).  As for the other entry points: caller-owned device memory, 256-byte
  * aligned, zeroed once before first use (and again after MOE_ERR_TIMEOUT),
  * not shared by calls that overlap on the GPU -- two streams, or two captured
- * graphs that may run at the same time, need one each.  Its first word is the
- * device error word (moe_read_device_error).
+ * graphs that may run at the same time, need one each, and these bytes of it
+ * overlap no other operand.  Its first word is the device error word
+ * (moe_read_device_error).
  */
 size_t moe_grouped_workspace_size(void);
 

@@ -815,3 +815,31 @@ def test_fp8_scales_with_a_subnormal_product(cuda_device, ws, counts, n_in):
     codes.zero_()
     moe.grouped_mm_fp8(codes, sx, w, sw, off, y, ws)
     assert bool((y == 0).all()) and moe.read_device_error(ws) == 0
+
+
+def test_operands_in_the_workspace_are_refused(cuda_device):
+    """The workspace is written while the operands are read: none of them may lie in it; behind its bytes they may."""
+    size = moe.grouped_workspace_size()
+    buf = torch.zeros(size + (1 << 16), dtype=torch.uint8, device=cuda_device)
+    part = buf[size - 8192:size].view(BF)
+    x, y, w = part[:512].view(8, 64), torch.zeros(8, 64, dtype=BF, device=cuda_device), part[:4096].view(1, 64, 64)
+    free, sx, sw = torch.ones(1, 64, 64, dtype=BF, device=cuda_device), torch.ones(1, 8, device=cuda_device), \
+        torch.ones(1, 1, 1, device=cuda_device)
+    off = buf[size - 8:size].view(torch.int32)
+    codes, wide = torch.zeros(8, 64, dtype=torch.uint8, device=cuda_device), buf[size - 4096:size].view(1, 64, 64)
+    calls = {
+        "x": [lambda: moe.grouped_mm(x, free, None, y, buf), lambda: moe.grouped_mm_dw(y, x, None, free, buf)],
+        "w": [lambda: moe.grouped_mm(y.clone(), w, None, y, buf), lambda: moe.grouped_mm_dx(y.clone(), w, None, y, buf),
+              lambda: moe.grouped_mm_fp8(codes, sx, wide, sw, None, y, buf)],
+        "dy": [lambda: moe.grouped_mm_dx(x, free, None, y, buf), lambda: moe.grouped_mm_dw(x, y, None, free, buf)],
+        "expert_offsets": [lambda: moe.grouped_mm(y.clone(), free, off, y, buf)],
+        "x_scales": [lambda: moe.grouped_mm_fp8(codes, part[:16].view(FP).view(1, 8), wide.clone(), sw, None, y, buf)],
+        "w_scales": [lambda: moe.grouped_mm_fp8(codes, sx, wide.clone(), part[:2].view(FP).view(1, 1, 1), None, y, buf)]}
+    for name, group in calls.items():
+        for call in group:
+            with pytest.raises(moe.MoEError, match=rf"ws overlaps {name}\)"):
+                call()
+    after = buf[size:size + 1024].view(BF).view(8, 64)
+    after.fill_(1)
+    moe.grouped_mm(after, free, None, y, buf)
+    assert bool((y == 64).all()) and moe.read_device_error(buf) == 0
