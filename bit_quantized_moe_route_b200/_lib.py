@@ -304,6 +304,12 @@ def _rows_arg(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     return t.stride(0) if rows > 1 else max(cols, 1)
 
 
+def _row_count(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
+    return t.size(0)
+
+
 def _one_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
     if not first.is_cuda:
         raise ValueError("expected a CUDA tensor")
@@ -352,7 +358,7 @@ def grouped_mm(x, w, expert_offsets, y, ws, stream=None):
     if w.dim() != 3 or w.dtype != x.dtype:
         raise ValueError("w must be [E, n_out, n_in] of x's type")
     E, n_out, n_in = w.shape
-    R = x.shape[0]
+    R = _row_count(x, "x")
     ld_x, ld_y = _rows_arg(x, "x", R, n_in), _rows_arg(y, "y", R, n_out)
     d = _gmm_dims(x.dtype, y.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(x, w, expert_offsets, y, ws)
@@ -365,7 +371,7 @@ def grouped_mm_dx(dy, w, expert_offsets, dx, ws, stream=None):
     if w.dim() != 3 or w.dtype != dy.dtype:
         raise ValueError("w must be [E, n_out, n_in] of dy's type")
     E, n_out, n_in = w.shape
-    R = dy.shape[0]
+    R = _row_count(dy, "dy")
     ld_dy, ld_dx = _rows_arg(dy, "dy", R, n_out), _rows_arg(dx, "dx", R, n_in)
     d = _gmm_dims(dy.dtype, dx.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(dy, w, expert_offsets, dx, ws)
@@ -379,7 +385,7 @@ def grouped_mm_dw(dy, x, expert_offsets, dw, ws, stream=None):
     if dw.dim() != 3 or x.dtype != dy.dtype:
         raise ValueError("dw must be [E, n_out, n_in], x and dy of one type")
     E, n_out, n_in = dw.shape
-    R = dy.shape[0]
+    R = _row_count(dy, "dy")
     ld_dy, ld_x = _rows_arg(dy, "dy", R, n_out), _rows_arg(x, "x", R, n_in)
     d = _gmm_dims(x.dtype, dw.dtype, expert_offsets, E, R, n_out, n_in, ws)
     _one_device(dy, x, expert_offsets, dw, ws)
@@ -399,7 +405,7 @@ def grouped_mm_fp8(x, x_scales, w, w_scales, expert_offsets, y, ws, stream=None)
     if w.dim() != 3 or w.dtype not in _FP8_TYPES or x.dtype not in _FP8_TYPES:
         raise ValueError("x and w must be e4m3 codes (float8_e4m3fn or uint8), w [E, n_out, n_in]")
     E, n_out, n_in = w.shape
-    R = x.shape[0]
+    R = _row_count(x, "x")
     gi, go = (n_in + 127) // 128, (n_out + 127) // 128
     if x_scales.dtype != torch.float32 or tuple(x_scales.shape) != (gi, R):
         raise ValueError(f"x_scales must be float32 [{gi}, {R}]")

@@ -121,3 +121,23 @@ def test_binding_refuses(lib):
     bad("codes", moe.quant_fp8, x, c[:7], sx)
     bad("scales", moe.quant_fp8, x, c, sx.t())
     bad("type", moe.quant_fp8, x.float(), c, sx)
+
+
+@pytest.mark.parametrize("shape", [(), (64,), (2, 4, 32), (0,)])
+def test_binding_refuses_what_is_no_matrix(lib, shape):
+    import bit_quantized_moe_route_b200 as moe
+    bf = torch.bfloat16
+    x, w, off, ws = torch.zeros(shape, dtype=bf), torch.zeros(4, 64, 32, dtype=bf), torch.zeros(5, dtype=torch.int32), \
+        torch.zeros(64, dtype=torch.uint8)
+    y, codes = torch.zeros(8, 64, dtype=bf), torch.zeros(8, 32, dtype=torch.uint8)
+    sx, sw, wc = torch.zeros(1, 8), torch.zeros(4, 1, 1), torch.zeros(4, 64, 32, dtype=torch.uint8)
+    for call, args in ((moe.grouped_mm, (x, w, off, y, ws)), (moe.grouped_mm, (y[:, :32], w, off, x, ws)),
+                       (moe.grouped_mm_dx, (x, w, off, y[:, :32], ws)), (moe.grouped_mm_dx, (y, w, off, x, ws)),
+                       (moe.grouped_mm_dw, (x, y[:, :32], off, w, ws)), (moe.grouped_mm_dw, (y, x, off, w, ws)),
+                       (moe.grouped_mm_dw, (y, y[:, :32], off, x, ws)), (moe.grouped_mm_fp8, (x.byte(), sx, wc, sw, off, y, ws)),
+                       (moe.grouped_mm_fp8, (codes, sx, wc, sw, off, x, ws)), (moe.quant_fp8, (x, codes, sx)),
+                       (moe.grouped_mm, (y[:, :32], x, off, y, ws))):
+        if len(shape) == 3 and any(a is x for a in args[1:4]) and call is not moe.grouped_mm_fp8:
+            continue                                              # a stack of matrices where one is taken
+        with pytest.raises(ValueError, match="must be"):
+            call(*args)
