@@ -843,3 +843,74 @@ def test_operands_in_the_workspace_are_refused(cuda_device):
     after.fill_(1)
     moe.grouped_mm(after, free, None, y, buf)
     assert bool((y == 64).all()) and moe.read_device_error(buf) == 0
+
+
+def whole(g, dtype, most, *shape):
+    return torch.randint(-most, most + 1, shape, generator=g, device=g.device).to(dtype)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("length", [8192, 8191, 65536, 65535])
+def test_long_sums_exactly(cuda_device, ws, op, dtype, length):
+    """Whole numbers up to 4: every partial sum is one below 2^20 and exact in fp32, however it is taken, so that a
+    product lost or counted twice anywhere in a long sum shows."""
+    g, wide, rows = gen(length, cuda_device), 264, 77
+    off = offsets_of([30, 0, 47], cuda_device)
+    if op == "dw":
+        off = offsets_of([length - 4100, 0, 4100], cuda_device)
+        dy, x = whole(g, dtype, 4, length, wide), whole(g, dtype, 4, length, 135)
+        y = torch.empty(3, wide, 135, dtype=FP, device=cuda_device)
+        moe.grouped_mm_dw(dy, x, off, y, ws)
+        ref, _ = reference("dw", dy, x, off, 3)
+    elif op == "mm":
+        x, w = whole(g, dtype, 4, rows, length), whole(g, dtype, 4, 3, wide, length)
+        y = torch.empty(rows, wide, dtype=FP, device=cuda_device)
+        moe.grouped_mm(x, w, off, y, ws)
+        ref, _ = reference("mm", x, w, off, 3)
+    else:
+        dy, w = whole(g, dtype, 4, rows, length), whole(g, dtype, 4, 3, length, wide - length % 2)
+        y = torch.empty(rows, wide - length % 2, dtype=FP, device=cuda_device)
+        moe.grouped_mm_dx(dy, w, off, y, ws)
+        ref, _ = reference("dx", dy, w, off, 3)
+    assert moe.read_device_error(ws) == 0
+    assert torch.equal(y.double(), ref)
+
+
+@pytest.mark.parametrize("n_in,pitch", [(128, 32776), (129, 32771)])
+def test_rows_beyond_4_gib_exactly(cuda_device, ws, n_in, pitch):
+    """Rows whose byte offsets pass 32 bits, of -1, 0 and 1: sums are exact in fp32 and, of 128 products, in bf16."""
+    rows, n_out, dev = 70000, 40, cuda_device
+    g, counts = gen(6, dev), [60000, 0, 10000]
+    x = torch.empty(rows * pitch, dtype=BF, device=dev).view(rows, pitch)[:, 5 if n_in == 129 else 8:][:, :n_in]
+    x.copy_(whole(g, BF, 1, rows, n_in))
+    y = torch.empty(rows * pitch, dtype=BF, device=dev).view(rows, pitch)[:, :n_out]
+    off, w, dy = offsets_of(counts, dev), whole(g, BF, 1, 3, n_out, n_in), whole(g, BF, 1, rows, n_out)
+    dw, dx = torch.empty(3, n_out, n_in, dtype=FP, device=dev), y.as_strided((rows, n_in), (pitch, 1), 64)
+    moe.grouped_mm(x, w, off, y, ws)
+    moe.grouped_mm_dx(dy, w, off, dx, ws)
+    moe.grouped_mm_dw(dy, x, off, dw, ws)
+    assert moe.read_device_error(ws) == 0
+    for op, got, a, b in (("mm", y, x, w), ("dx", dx, dy, w), ("dw", dw, dy, x)):
+        assert torch.equal(got.double(), reference(op, a, b, off, 3)[0]), op
+
+
+@pytest.mark.parametrize("counts,n_in,n_out", [([70], 65536, 136), ([70], 65535, 136), ([900], 65536, 264),
+                                               ([20, 0, 50, 3], 8192, 129)])
+def test_fp8_long_sums_exactly(cuda_device, ws, counts, n_in, n_out):
+    """Whole numbers up to 4 and scales of 1/2, 1 and 2: sums up to 2^22 in steps of a quarter, exact in fp32."""
+    g, rows, E, dev = gen(n_in + n_out, cuda_device), sum(counts), len(counts), cuda_device
+    gi, go = (n_in + 127) // 128, (n_out + 127) // 128
+
+    def codes(*shape):
+        return whole(g, FP, 4, *shape).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    def scales(*shape):
+        return 2.0 ** whole(g, FP, 1, *shape)                     # 1/2, 1, 2
+
+    x, w, sx, sw = codes(rows, n_in), codes(E, n_out, n_in), scales(gi, rows), scales(E, go, gi)
+    y = torch.empty(rows, n_out, dtype=FP, device=dev)
+    off = offsets_of(counts, dev)
+    moe.grouped_mm_fp8(x, sx, w, sw, off, y, ws)
+    assert moe.read_device_error(ws) == 0
+    assert torch.equal(y.double(), reference("mm", fp8_wide(x, sx), fp8_wide(w, sw), off, E)[0])
