@@ -54,15 +54,17 @@
 // than L2 holds: 32,768 rows over 32 experts took 870 us that way, 588 dealt
 // out).  All but the last one to two tiles per pair are dealt whole, and as
 // many of the rest's halves as there are for all pairs.  What is then left is
-// cut evenly, a number of pairs to each, or (dw, whose tiles differ in length,
-// and few tiles) by steps: their steps are one line, cut so that every pair
-// has the same cost in all.  A tile that a cut goes through is summed by
+// dealt whole too, or cut evenly, a number of pairs to each, or (dw, whose tiles
+// differ in length, and few tiles) cut by steps: their steps are one line, cut
+// so that every pair has the same cost in all.  Which, is what steps and joins
+// cost (gu_plan): one 8-bit token, 4096 -> 2048, is eight tiles in four parts
+// each; one token over eight 16-bit experts of that size is 64 tiles dealt
+// whole, with ten of the 74 pairs idle.  A tile that a cut goes through is summed by
 // the pairs that hold parts of it: each writes its fp32 partial sums to the
 // workspace and counts itself in; the last one adds the partials in the
 // pieces' order (so the result does not depend on who was last) and writes
-// the outputs.  No pair waits for another.  This keeps every SM busy when
-// there are few tiles (one token over eight experts: 64 tiles for 74 pairs),
-// and costs at most two partial tiles per pair.
+// the outputs.  No pair waits for another.  This costs at most two partial
+// tiles per pair.
 //
 // Tensor memory is a ring of eight slots of 64 columns; a sum takes one, two
 // or four of them, so that narrow tiles have up to eight sums in flight
@@ -569,14 +571,17 @@ MOE_DEV int gu_plan(const GmmProblem& p, GuLine& l, int tid, int cols, int split
   // What is left (halves of tiles for MT = 2; at most kGuTailMost - 1): as many
   // as there are for every pair are dealt too, and each of the others is cut
   // evenly, for at most as many pairs as there are, or all of it is the line,
-  // whichever costs less.  Measured, in us, for tiles of np columns: a step
+  // whichever costs less.  Measured, in us, for tiles of np columns, with
+  // operands in L2 (a step whose weights come from HBM takes longer): a step
   // 0.145 + np / 3000 (8-bit of over 64 columns, which hand over every other
   // step: 0.45; ANY: 0.45 + np / 470); joining k parts 0.4 + np / 62 + k (0.2 +
   // np / 154).  E.g. 128 steps of 32 columns: whole 33.0, in four 18.2, eight
   // 17.2, sixteen 20.1; 19 steps of 240: whole 13.6, in two 20.7.  dw, whose
   // tiles differ in length:
-  // dealt if the longest have at most 40 steps (256 rows over ten experts: 179 us,
-  // on the line 265), else the line.
+  // dealt if the longest have at most 40 steps, else the line.  Dealt / line, us,
+  // for ten experts of 4096 -> 2048: 4 steps 85 / 105, 20 steps 163 / 178, 40 steps
+  // 301 / 314, 80 steps 692 / 696, 160 steps 1,340 / 1,289; six of 1024 -> 1024: 4
+  // steps 18 / 32, 40 steps 60 / 67, 80 steps 104 / 102, 160 steps 209 / 179.
   int halves = 0, each_in = 0;
   {
     const int q = rest / cols, r = rest - q * cols;
